@@ -7,7 +7,10 @@ kernels.  There is no fallback: if the shared library is missing or cannot be
 loaded, importing this package raises.
 
 ``attention()`` is a convenience wrapper that allocates the outputs with
-PyTorch and calls ``attn_fwd``.
+PyTorch and calls ``attn_fwd``.  The serving operators have such wrappers too:
+``Rope`` / ``qk_norm_rope``, ``KVCache`` / ``kv_write`` / ``kv_read``,
+``attention_varlen`` and ``attention_paged`` take torch tensors, check them,
+and allocate outputs and workspace.
 """
 from __future__ import annotations
 
@@ -22,12 +25,15 @@ __all__ = [
     "attn_fwd_schedule", "attn_hadamard_quant_fp8_noalloc", "attn_fwd_splitkv", "attn_splitkv_workspace_bytes",
     "attn_combine", "attn_kv_tile_count_window", "attn_tile_kind_window", "attn_gemm_add", "lib_path", "EXPORTS",
     "attn_debug_map_cache_stats", "attn_fwd_part", "attn_shard_units", "attention_shard", "attn_fwd_host",
+    "attn_rope_freqs", "attn_qk_norm_rope", "attn_kv_write", "attn_kv_read", "attn_fwd_varlen",
+    "attn_fwd_varlen_workspace_bytes", "attn_fwd_paged", "attn_fwd_paged_workspace_bytes", "rope_freqs", "Rope",
+    "KVCache", "qk_norm_rope", "kv_write", "kv_read", "attention_varlen", "attention_paged",
 ]
 
 ATTN_BF16 = 0
 ATTN_FP8_E4M3 = 1
 STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED", 3: "ATTN_ERR_MISALIGNED",
-          4: "ATTN_ERR_CUDA", 5: "ATTN_ERR_DEVICE_TIMEOUT"}
+          4: "ATTN_ERR_CUDA", 5: "ATTN_ERR_DEVICE_TIMEOUT", 6: "ATTN_ERR_DEVICE_INDEX"}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libattn.so")
@@ -39,7 +45,8 @@ EXPORTS = (
     "attn_debug_unsatisfied_wait", "attn_debug_exp2", "attn_hadamard_quant_fp8_noalloc", "attn_fwd_schedule",
     "attn_fwd_splitkv", "attn_splitkv_workspace_bytes", "attn_combine", "attn_kv_tile_count_window",
     "attn_tile_kind_window", "attn_gemm_add", "attn_debug_map_cache_stats", "attn_fwd_part", "attn_shard_units",
-    "attn_fwd_host",
+    "attn_fwd_host", "attn_rope_freqs", "attn_qk_norm_rope", "attn_kv_write", "attn_kv_read", "attn_fwd_varlen",
+    "attn_fwd_varlen_workspace_bytes", "attn_fwd_paged", "attn_fwd_paged_workspace_bytes",
 )
 
 if not os.path.exists(lib_path):
@@ -92,6 +99,37 @@ _lib.attn_gemm_add.argtypes = [_vp] * 4 + [_I] * 3 + [_vp]
 _lib.attn_gemm_add.restype = _I
 _lib.attn_debug_map_cache_stats.argtypes = [ctypes.POINTER(ctypes.c_ulonglong)] * 2
 _lib.attn_debug_map_cache_stats.restype = _I
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k_pages", _vp), ("v_pages", _vp), ("k_exp", _vp), ("v_exp", _vp), ("n_pages", _I),
+                ("page_size", _I), ("Hkv", _I), ("d", _I), ("dtype", _I)]
+
+
+class _RopeStruct(ctypes.Structure):
+    _fields_ = [("q_weight", _vp), ("k_weight", _vp), ("freqs", _vp), ("eps", _F), ("amplitude", _F),
+                ("rot_dim", _I), ("interleaved", _I)]
+
+
+_D = ctypes.c_double
+_pc, _pr = ctypes.POINTER(_CacheStruct), ctypes.POINTER(_RopeStruct)
+_lib.attn_rope_freqs.argtypes = [ctypes.POINTER(_D), _I, _D, _I, _D, _D, _D, _D, ctypes.POINTER(_F)]
+_lib.attn_rope_freqs.restype = _I
+_lib.attn_qk_norm_rope.argtypes = [_vp] * 4 + [_LL, _I, _I, _I] + [_LL] * 4 + [_vp, _pr, _vp]
+_lib.attn_qk_norm_rope.restype = _I
+_lib.attn_kv_write.argtypes = [_pc, _vp, _vp, _LL, _LL, _LL, _vp, _pr, _vp, _vp, _vp, _I, _LL, _LL, _vp]
+_lib.attn_kv_write.restype = _I
+_lib.attn_kv_read.argtypes = [_pc, _vp, _I, _vp, _I, _vp, _vp, _LL, _vp]
+_lib.attn_kv_read.restype = _I
+_lib.attn_fwd_varlen_workspace_bytes.argtypes = [_I] * 5
+_lib.attn_fwd_varlen_workspace_bytes.restype = _LL
+_lib.attn_fwd_varlen.argtypes = [_vp] * 5 + [_I] * 3 + [_vp] * 2 + [_I] * 3 + [_LL] * 3 + [_I, _F, _vp, _LL, _vp]
+_lib.attn_fwd_varlen.restype = _I
+_lib.attn_fwd_paged_workspace_bytes.argtypes = [_pc] + [_I] * 6
+_lib.attn_fwd_paged_workspace_bytes.restype = _LL
+_lib.attn_fwd_paged.argtypes = [_vp, _pc, _vp, _vp, _I, _I, _I, _vp, _vp, _I, _vp, _I, _I, _LL, _I, _F, _I, _vp, _LL,
+                                _vp]
+_lib.attn_fwd_paged.restype = _I
 
 
 class AttnError(RuntimeError):
@@ -283,4 +321,310 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None, return_
     o = torch.empty_like(q)
     lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device) if return_lse else None
     attn_fwd(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, causal, scale, ATTN_BF16, stream)
+    return (o, lse) if return_lse else o
+
+
+# ------------------------------------------------------------------ serving
+ROPE_KINDS = {"plain": 0, "linear": 1, "ntk": 2, "bands": 3}
+
+
+def attn_rope_freqs(rot_dim, base, kind=0, factor=1.0, trained_len=0.0, fast_turns=32.0, slow_turns=1.0):
+    """(frequencies as a list of rot_dim / 2 floats, amplitude); host only."""
+    buf, amp = (_D * max(int(rot_dim) // 2, 1))(), _F(0.0)
+    _check(_lib.attn_rope_freqs(buf, int(rot_dim), float(base), int(kind), float(factor), float(trained_len),
+                                float(fast_turns), float(slow_turns), ctypes.byref(amp)), "attn_rope_freqs", True)
+    return list(buf), amp.value
+
+
+def attn_qk_norm_rope(q, k, q_out, k_out, T, Hq, Hkv, d, q_stride, k_stride, q_out_stride, k_out_stride, positions,
+                      rope, stream=None, raise_on_error=True):
+    rc = _lib.attn_qk_norm_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), T, Hq, Hkv, d, q_stride, k_stride,
+                                q_out_stride, k_out_stride, _ptr(positions), rope, _stream(stream))
+    return _check(rc, "attn_qk_norm_rope", raise_on_error)
+
+
+def attn_kv_write(cache, k, v, T, k_stride, v_stride, slots, rope=None, positions=None, q=None, q_out=None, Hq=0,
+                  q_stride=0, q_out_stride=0, stream=None, raise_on_error=True):
+    rc = _lib.attn_kv_write(cache, _ptr(k), _ptr(v), T, k_stride, v_stride, _ptr(slots), rope, _ptr(positions), _ptr(q),
+                            _ptr(q_out), Hq, q_stride, q_out_stride, _stream(stream))
+    return _check(rc, "attn_kv_write", raise_on_error)
+
+
+def attn_kv_read(cache, table, table_width, cu, n_seqs, k, v, T, stream=None, raise_on_error=True):
+    rc = _lib.attn_kv_read(cache, _ptr(table), table_width, _ptr(cu), n_seqs, _ptr(k), _ptr(v), T, _stream(stream))
+    return _check(rc, "attn_kv_read", raise_on_error)
+
+
+def attn_fwd_varlen_workspace_bytes(Tq, n_seqs, Hq, Hkv, d) -> int:
+    return int(_lib.attn_fwd_varlen_workspace_bytes(Tq, n_seqs, Hq, Hkv, d))
+
+
+def attn_fwd_varlen(q, k, v, o, lse, Tq, Tk, n_seqs, cu_q, cu_k, Hq, Hkv, d, q_stride, k_stride, v_stride, causal,
+                    scale, workspace, workspace_bytes, stream=None, raise_on_error=True):
+    rc = _lib.attn_fwd_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), Tq, Tk, n_seqs, _ptr(cu_q), _ptr(cu_k),
+                              Hq, Hkv, d, q_stride, k_stride, v_stride, int(causal), scale, _ptr(workspace),
+                              workspace_bytes, _stream(stream))
+    return _check(rc, "attn_fwd_varlen", raise_on_error)
+
+
+def attn_fwd_paged_workspace_bytes(cache, Tq, n_seqs, max_q, Hq, max_kv, n_splits=0) -> int:
+    return int(_lib.attn_fwd_paged_workspace_bytes(cache, Tq, n_seqs, max_q, Hq, max_kv, n_splits))
+
+
+def attn_fwd_paged(q, cache, o, lse, Tq, n_seqs, max_q, cu_q, table, table_width, kv_lens, max_kv, Hq, q_stride, causal,
+                   scale, n_splits, workspace, workspace_bytes, stream=None, raise_on_error=True):
+    rc = _lib.attn_fwd_paged(_ptr(q), cache, _ptr(o), _ptr(lse), Tq, n_seqs, max_q, _ptr(cu_q), _ptr(table),
+                             table_width, _ptr(kv_lens), max_kv, Hq, q_stride, int(causal), scale, n_splits,
+                             _ptr(workspace), workspace_bytes, _stream(stream))
+    return _check(rc, "attn_fwd_paged", raise_on_error)
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _on_current_device(*tensors):
+    """Every tensor is on the current CUDA device (the library launches there)."""
+    import torch
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != cur):
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
+
+
+def _rows(x, name):
+    """Token stride of a bf16 [T, H, d] tensor whose heads are contiguous."""
+    import torch
+    if x.dim() != 3 or x.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a bf16 tensor [T, H, d]")
+    T, H, d = x.shape
+    if x.numel() == 0:
+        return H * d
+    st = x.stride()
+    if (st[2] != 1 and d > 1) or (st[1] != d and H > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return st[0] if T > 1 else H * d
+
+
+def _index(x, name, dtype, n=None, dim=1):
+    import torch
+    want = getattr(torch, dtype)
+    if x.dtype != want or x.dim() != dim or not x.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor of {dim} dimension(s)")
+    if n is not None and x.shape[0] != n:
+        raise ValueError(f"{name} has {x.shape[0]} entries, {n} are needed")
+
+
+def _on_stream(stream, *tensors):
+    """Tensors allocated here belong to the current stream: tell the allocator of another one that uses them."""
+    if stream is None:
+        return
+    import torch
+    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+    if s != torch.cuda.current_stream():
+        s.wait_stream(torch.cuda.current_stream())  # their memory may still be in use there
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
+
+
+def rope_freqs(rot_dim, base, kind="plain", factor=1.0, trained_len=0.0, fast_turns=32.0, slow_turns=1.0,
+               device="cuda"):
+    """(frequencies as an fp64 tensor on `device`, amplitude) for Rope()."""
+    import torch
+    f, amp = attn_rope_freqs(rot_dim, base, ROPE_KINDS[kind], factor, trained_len, fast_turns, slow_turns)
+    return torch.tensor(f, dtype=torch.float64, device=device), amp
+
+
+class Rope:
+    """Norm weights and rotation of queries and keys (attn_rope_t); keeps its tensors alive."""
+
+    def __init__(self, freqs=None, rot_dim=0, interleaved=False, amplitude=1.0, q_weight=None, k_weight=None,
+                 eps=1e-6):
+        import torch
+        _need(rot_dim == 0 or freqs is not None, "freqs are needed where rot_dim > 0")
+        if freqs is not None and rot_dim > 0:
+            _index(freqs, "freqs", "float64", rot_dim // 2)
+        d = None
+        for w in (q_weight, k_weight):
+            if w is not None:
+                if w.dtype != torch.bfloat16 or w.dim() != 1 or not w.is_contiguous():
+                    raise TypeError("norm weights must be contiguous bf16 tensors [d]")
+                _need(d is None or w.shape[0] == d, "the norm weights differ in length")
+                d = w.shape[0]
+        self.d = d  # the head size the weights are for, None without weights
+        self.tensors = (freqs, q_weight, k_weight)
+        self.rot_dim = rot_dim
+        self.struct = _RopeStruct(_ptr(q_weight), _ptr(k_weight), _ptr(freqs) if rot_dim > 0 else None, eps, amplitude,
+                                  rot_dim, int(interleaved))
+
+
+class KVCache:
+    """A paged key/value cache (attn_kv_cache_t) over torch tensors, which it keeps alive: k_pages and
+    v_pages [n_pages, page_size, Hkv, d] in bf16 or float8_e4m3fn (or uint8 codes); for e4m3 the exponent
+    bytes k_exp and v_exp [n_pages, page_size, Hkv] in uint8."""
+
+    def __init__(self, k_pages, v_pages, k_exp=None, v_exp=None):
+        import torch
+        if k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8) or v_pages.dtype != k_pages.dtype:
+            raise TypeError("k_pages and v_pages must both be bf16, float8_e4m3fn or uint8")
+        _need(k_pages.dim() == 4 and k_pages.shape == v_pages.shape, "k_pages and v_pages must be [n_pages, page_size, Hkv, d]")
+        e4m3 = k_pages.dtype != torch.bfloat16
+        for e in (k_exp, v_exp):
+            _need((e is not None) == e4m3, "an e4m3 cache needs k_exp and v_exp, a bf16 cache has none")
+            if e is not None and (e.dtype != torch.uint8 or e.shape != k_pages.shape[:3]):
+                raise TypeError("k_exp and v_exp must be uint8 [n_pages, page_size, Hkv]")
+        for t in (k_pages, v_pages, k_exp, v_exp):
+            _need(t is None or t.is_contiguous(), "the cache's tensors must be contiguous")
+        self.tensors = (k_pages, v_pages, k_exp, v_exp)
+        self.n_pages, self.page_size, self.Hkv, self.d = k_pages.shape
+        self.struct = _CacheStruct(_ptr(k_pages), _ptr(v_pages), _ptr(k_exp), _ptr(v_exp), self.n_pages,
+                                   self.page_size, self.Hkv, self.d, ATTN_FP8_E4M3 if e4m3 else ATTN_BF16)
+
+
+def _check_rope_use(rope, d, positions, T):
+    _need(rope.d is None or rope.d == d, "the norm weights are for another head size")
+    if rope.rot_dim > 0:
+        _need(positions is not None, "positions are needed where rot_dim > 0")
+        _index(positions, "positions", "int64", T)
+
+
+def qk_norm_rope(q, k, positions, rope, q_out=None, k_out=None, stream=None):
+    """q [T, Hq, d] and k [T, Hkv, d] (bf16, slices of a fused projection allowed) normed and rotated;
+    returns (q_out, k_out), new contiguous tensors unless given (q_out=q and k_out=k work in place)."""
+    import torch
+    T, Hq, d = q.shape
+    Hkv = k.shape[1]
+    _need(k.shape[0] == T and k.shape[2] == d, "q and k must have the same tokens and head size")
+    _check_rope_use(rope, d, positions, T)
+    _on_current_device(q, k, positions, q_out, k_out, *rope.tensors)
+    new = []
+    if q_out is None:
+        q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
+        new.append(q_out)
+    if k_out is None:
+        k_out = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=q.device)
+        new.append(k_out)
+    _need(q_out.shape == q.shape and k_out.shape == k.shape, "the outputs must have the inputs' shapes")
+    _on_stream(stream, *new)
+    attn_qk_norm_rope(q, k, q_out, k_out, T, Hq, Hkv, d, _rows(q, "q"), _rows(k, "k"), _rows(q_out, "q_out"),
+                      _rows(k_out, "k_out"), positions, rope.struct, stream)
+    return q_out, k_out
+
+
+def kv_write(cache, k, v, slots, q=None, positions=None, rope=None, q_out=None, stream=None):
+    """Keys and values [T, Hkv, d] (bf16) into the cache's slots (int64 [T], negative: skipped).  With rope the
+    keys are normed and rotated on the way, and so are the queries q [T, Hq, d], which are returned."""
+    import torch
+    T = k.shape[0]
+    _need(k.shape == v.shape == (T, cache.Hkv, cache.d), "k and v must be [T, Hkv, d] of the cache")
+    _index(slots, "slots", "int64", T)
+    _need(rope is not None or q is None, "queries only take part where rope is given")
+    _on_current_device(k, v, slots, q, positions, q_out, *cache.tensors, *(rope.tensors if rope is not None else ()))
+    if rope is not None:
+        _check_rope_use(rope, cache.d, positions, T)
+    Hq = qs = qos = 0
+    if q is not None:
+        Hq = q.shape[1]
+        _need(q.shape[0] == T and q.shape[2] == cache.d, "q must have k's tokens and head size")
+        if q_out is None:
+            q_out = torch.empty((T, Hq, cache.d), dtype=torch.bfloat16, device=q.device)
+            _on_stream(stream, q_out)
+        _need(q_out.shape == q.shape, "q_out must have q's shape")
+        qs, qos = _rows(q, "q"), _rows(q_out, "q_out")
+    attn_kv_write(cache.struct, k, v, T, _rows(k, "k"), _rows(v, "v"), slots, rope.struct if rope is not None else None,
+                  positions, q, q_out, Hq, qs, qos, stream)
+    return q_out
+
+
+def kv_read(cache, table, cu, T, k_out=None, v_out=None, stream=None):
+    """The cached tokens of each sequence (pages table[s], int32; boundaries cu of the T output rows, int32
+    [n_seqs + 1]) as packed bf16 keys and values [T, Hkv, d]."""
+    import torch
+    n = table.shape[0]
+    _index(table, "table", "int32", dim=2)
+    _index(cu, "cu", "int32", n + 1)
+    _on_current_device(table, cu, k_out, v_out, *cache.tensors)
+    shape, new = (T, cache.Hkv, cache.d), []
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=table.device)
+        new.append(k_out)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=table.device)
+        new.append(v_out)
+    for t in (k_out, v_out):
+        _need(tuple(t.shape) == shape and t.dtype == torch.bfloat16 and t.is_contiguous(),
+              "k_out and v_out must be contiguous bf16 [T, Hkv, d]")
+    _on_stream(stream, *new)
+    attn_kv_read(cache.struct, table, table.shape[1], cu, n, k_out, v_out, T, stream)
+    return k_out, v_out
+
+
+def _outputs(q, o, lse, return_lse):
+    """(o, lse, tensors made here)"""
+    import torch
+    T, H, d = q.shape
+    new = []
+    if o is None:
+        o = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
+        new.append(o)
+    if lse is None and return_lse:
+        lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+        new.append(lse)
+    _need(o.shape == q.shape and o.dtype == torch.bfloat16 and o.is_contiguous(), "o must be contiguous bf16 like q")
+    _need(lse is None or (tuple(lse.shape) == (H, T) and lse.dtype == torch.float32 and lse.is_contiguous()),
+          "lse must be contiguous fp32 [Hq, T]")
+    return o, lse, new
+
+
+def attention_varlen(q, k, v, cu_q, cu_k, causal: bool = False, scale: float | None = None, return_lse: bool = True,
+                     o=None, lse=None, stream=None):
+    """O [Tq, Hq, d] (and LSE [Hq, Tq]) of packed sequences: q [Tq, Hq, d], k/v [Tk, Hkv, d] (bf16, slices of a
+    fused projection allowed), boundaries cu_q, cu_k int32 [n_seqs + 1].  Rows outside every sequence are
+    not written."""
+    import torch
+    Tq, Hq, d = q.shape
+    Tk, Hkv, _ = k.shape
+    _need(k.shape == v.shape and k.shape[2] == d, "k and v must have the same shape, and q's head size")
+    n = cu_q.shape[0] - 1
+    _index(cu_q, "cu_q", "int32")
+    _index(cu_k, "cu_k", "int32", n + 1)
+    _on_current_device(q, k, v, cu_q, cu_k, o, lse)
+    o, lse, new = _outputs(q, o, lse, return_lse)
+    nbytes = attn_fwd_varlen_workspace_bytes(Tq, n, Hq, Hkv, d)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes > 0 else None
+    _on_stream(stream, ws, *new)
+    attn_fwd_varlen(q, k, v, o, lse, Tq, Tk, n, cu_q, cu_k, Hq, Hkv, d, _rows(q, "q"), _rows(k, "k"), _rows(v, "v"),
+                    causal, 1.0 / math.sqrt(d) if scale is None else scale, ws, max(nbytes, 0), stream)
+    return (o, lse) if return_lse else o
+
+
+def attention_paged(q, cache, table, kv_lens, cu_q=None, max_q=None, max_kv=None, causal: bool = True,
+                    scale: float | None = None, n_splits: int = 0, return_lse: bool = True, o=None, lse=None,
+                    stream=None):
+    """O [Tq, Hq, d] (and LSE [Hq, Tq]) of new tokens q over the cache, which holds them already: table int32
+    [n_seqs, width], kv_lens int32 [n_seqs] with the new tokens counted.  cu_q int32 [n_seqs + 1] gives the
+    sequences' rows of q and max_q bounds their number; without cu_q every sequence has Tq / n_seqs rows."""
+    import torch
+    Tq, Hq, d = q.shape
+    n = table.shape[0]
+    _need(d == cache.d, "q and the cache differ in head size")
+    _index(table, "table", "int32", dim=2)
+    _index(kv_lens, "kv_lens", "int32", n)
+    if cu_q is not None:
+        _index(cu_q, "cu_q", "int32", n + 1)
+        max_q = Tq if max_q is None else min(max_q, Tq)
+    else:
+        _need(n > 0 and Tq % n == 0 and max_q in (None, Tq // n), "without cu_q every sequence has Tq / n_seqs rows")
+        max_q = Tq // n
+    width = table.shape[1]
+    max_kv = width * cache.page_size if max_kv is None else max_kv
+    _on_current_device(q, table, kv_lens, cu_q, o, lse, *cache.tensors)
+    o, lse, new = _outputs(q, o, lse, return_lse)
+    nbytes = attn_fwd_paged_workspace_bytes(cache.struct, Tq, n, max_q, Hq, max_kv, n_splits)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes > 0 else None
+    _on_stream(stream, ws, *new)
+    attn_fwd_paged(q, cache.struct, o, lse, Tq, n, max_q, cu_q, table, width, kv_lens, max_kv, Hq, _rows(q, "q"), causal,
+                   1.0 / math.sqrt(d) if scale is None else scale, n_splits, ws, max(nbytes, 0), stream)
     return (o, lse) if return_lse else o

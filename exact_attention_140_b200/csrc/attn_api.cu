@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -17,6 +18,9 @@
 #include "combine.cuh"
 #include "fp8_prep.cuh"
 #include "gemm_add.cuh"
+#include "kv_cache.cuh"
+#include "paged_fwd.cuh"
+#include "ragged_plan.cuh"
 #include "tiles.h"
 
 namespace attn {
@@ -244,6 +248,32 @@ int encode_q_packed(CUtensorMap* m, const void* ptr, int B, int Nq, int Hkv, int
                                  (cuuint64_t)Nq * Hq * d * es};
   const cuuint32_t box[5] = {(cuuint32_t)(128 / es), (cuuint32_t)g, 1u, (cuuint32_t)(rows / g), 1u};
   return encode_cached(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, ptr, dims, strides, box);
+}
+
+// A packed [T, H, d] bf16 tensor with a token stride (elements), as a 4-D map
+// (d, H, T, 1) with a box of one head x `rows` tokens, or, for g > 1, as the
+// 5-D map (d, g, H / g, T, 1) of encode_q_packed.
+int encode_packed(CUtensorMap* m, const void* ptr, int T, int H, int d, long long stride, int rows) {
+  const cuuint64_t tok = (cuuint64_t)stride * 2;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T, 1};
+  const cuuint64_t strides[3] = {(cuuint64_t)d * 2, tok, tok * (cuuint64_t)T};
+  const cuuint32_t box[4] = {64u, 1u, (cuuint32_t)rows, 1u};
+  return encode_cached(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, ptr, dims, strides, box);
+}
+int encode_packed_groups(CUtensorMap* m, const void* ptr, int T, int H, int g, int d, long long stride, int rows) {
+  const cuuint64_t tok = (cuuint64_t)stride * 2;
+  const cuuint64_t dims[5] = {(cuuint64_t)d, (cuuint64_t)g, (cuuint64_t)(H / g), (cuuint64_t)T, 1};
+  const cuuint64_t strides[4] = {(cuuint64_t)d * 2, (cuuint64_t)g * d * 2, tok, tok * (cuuint64_t)T};
+  const cuuint32_t box[5] = {64u, (cuuint32_t)g, 1u, (cuuint32_t)(rows / g), 1u};
+  return encode_cached(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, ptr, dims, strides, box);
+}
+// Pages [n_pages, page_size, Hkv, d] of a bf16 cache: a box is one head x
+// `rows` tokens of one page.
+int encode_pages(CUtensorMap* m, const void* ptr, int n_pages, int page_size, int Hkv, int d, int rows) {
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)Hkv, (cuuint64_t)page_size, (cuuint64_t)n_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)Hkv * d * 2, (cuuint64_t)page_size * Hkv * d * 2};
+  const cuuint32_t box[4] = {64u, 1u, (cuuint32_t)rows, 1u};
+  return encode_cached(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, ptr, dims, strides, box);
 }
 
 // 2-D row-major bf16 matrix [rows, cols] as a 4-D map (cols, rows, 1, 1), box
@@ -775,6 +805,7 @@ const char* attn_status_string(int status) {
     case ATTN_ERR_MISALIGNED: return "tensor pointer not 16-byte aligned";
     case ATTN_ERR_CUDA: return "CUDA error";
     case ATTN_ERR_DEVICE_TIMEOUT: return "device-side wait timed out";
+    case ATTN_ERR_DEVICE_INDEX: return "index read from device memory outside its array";
     default: return "unknown status";
   }
 }
@@ -1103,7 +1134,8 @@ int attn_get_last_device_error(void* stream, unsigned int* detail) {
   if (word != 0 && cudaMemcpy(st->err, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
     return ATTN_ERR_CUDA;
   if (detail != nullptr) *detail = word;
-  return word != 0 ? ATTN_ERR_DEVICE_TIMEOUT : ATTN_OK;
+  if (word == 0) return ATTN_OK;
+  return word == kErrIndex ? ATTN_ERR_DEVICE_INDEX : ATTN_ERR_DEVICE_TIMEOUT;
 }
 
 int attn_debug_map_cache_stats(unsigned long long* hits, unsigned long long* encodes) {
@@ -1134,3 +1166,5 @@ int attn_debug_unsatisfied_wait(long long limit_ns, void* stream) {
 }
 
 }  // extern "C"
+
+#include "serving_api.cuh"

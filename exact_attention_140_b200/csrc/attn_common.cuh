@@ -9,6 +9,16 @@
 
 namespace attn {
 
+// Packed sequences (one-block-per-item kernel, RAGGED configurations): the
+// work items come from a list in device memory (ragged_plan_kernel).
+struct RaggedParams {
+  const int* plan;   // number of items, then from int 8 on items of 8 ints: seq, block, q0, nq, k0, nk, 0, 0
+  int max_items;     // items that the launch's grid has room for
+  int Tq;            // query tokens in all (lse rows)
+  const int* table;  // paged: page table [n_seqs, table_width]
+  int table_width, page_shift, n_pages;
+};
+
 struct FwdParams {
   void* o;          // [B, Nq, Hq, D] bf16
   float* lse;       // [B, Hq, Nq] fp32 or nullptr
@@ -47,8 +57,10 @@ struct FwdParams {
   const float* dv;
   unsigned int* err;            // device error word
   unsigned long long timeout_ns;
+  RaggedParams rg;
 };
 
+constexpr unsigned int kErrIndex = 2u;  // device error word: an index outside its array
 constexpr float kTau = 8.0f;  // lazy-rescale threshold, log2 units
 
 // Maximum of sl2 * s[c] over the visible columns c < nvis of N scores (the
@@ -80,8 +92,12 @@ __device__ __forceinline__ float masked_max_scaled(const uint32_t* sr, int nvis,
 }
 
 template <int D_, int BN_, int NQT_, int KST_, int VST_, bool CAUSAL_, bool FP8_, int EMU_ = 0,
-          int SB_ = (NQT_ == 1 ? 2 : 1), bool PSEP_ = false, int NS_ = 1, bool PACK_ = false, bool OST_ = false>
+          int SB_ = (NQT_ == 1 ? 2 : 1), bool PSEP_ = false, int NS_ = 1, bool PACK_ = false, bool OST_ = false,
+          int RAGGED_ = 0>
 struct FwdCfg {
+  // RAGGED (one-block-per-item kernel): 1 packed sequences, 2 packed queries
+  // over a paged cache; 0 the dense [B, N, H, d] tensors
+  static constexpr int RAGGED = RAGGED_;
   // PACK: the one-block-per-item kernel reads the head-packing factor from the
   // launch parameters (split-KV); otherwise it is compiled out
   static constexpr bool PACK = PACK_;

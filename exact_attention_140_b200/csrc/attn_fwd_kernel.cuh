@@ -80,7 +80,30 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = Cfg::PACK ? p.pack : 1;  // query heads stacked per tile row group
   int qb, hy, b, split;
-  if (p.band > 0) {
+  int nq = p.Nq, nk_all = p.Nk;                       // query rows and keys of the item's sequence
+  [[maybe_unused]] int q_base = 0, k_base = 0, seq = 0;  // RAGGED: its first query token and key, its index
+  if constexpr (Cfg::RAGGED != 0) {
+    // bands of heads as below, the listed items (longest first) within a band
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    split = (int)blockIdx.x % p.n_splits;
+    const int L = (int)blockIdx.x / p.n_splits, per = p.band * p.rg.max_items;
+    const int bi = L / per, within = L - bi * per;
+    const int bsz = p.nh - bi * p.band < p.band ? p.nh - bi * p.band : p.band;
+    const int item = within / bsz;
+    if (item >= __ldcg(p.rg.plan)) return;  // (from L2: written while this grid was being launched)
+    const int4 i0 = __ldcg(reinterpret_cast<const int4*>(p.rg.plan) + 2 + 2 * item);
+    const int2 i1 = __ldcg(reinterpret_cast<const int2*>(p.rg.plan) + 6 + 4 * item);
+    hy = bi * p.band + within % bsz;
+    b = 0;
+    seq = i0.x;
+    qb = i0.y;
+    q_base = i0.z;
+    nq = i0.w;
+    k_base = i1.x;
+    nk_all = i1.y;
+    if (split > 0 && split * p.kv_chunk >= nk_all) return;  // no such window
+  } else if (p.band > 0) {
     // longest-first within bands of (batch, head) pairs: a band's K/V stay in
     // L2 while its blocks run, and the hardware hands out blocks in this
     // order as SMs free up, so the long causal blocks do not end up last
@@ -102,8 +125,8 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
   }
   // key window of this block: [kv0, kv0 + nk), `shift` keys after it
   const int kv0 = split * p.kv_chunk;
-  const int nk = p.Nk - kv0 < p.kv_chunk ? p.Nk - kv0 : p.kv_chunk;
-  const int shift = p.Nk - kv0 - nk;
+  const int nk = nk_all - kv0 < p.kv_chunk ? nk_all - kv0 : p.kv_chunk;
+  const int shift = nk_all - kv0 - nk;
   const int kh = g > 1 ? hy : hy / p.group;
   const int q0 = qb * BM * NQT;
   int n_kv[NQT];
@@ -117,7 +140,7 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
   for (int t = 0; t < NQT; ++t) {
     int ia, ib;
     tile_rows(t, ia, ib);
-    n_kv[t] = kv_tile_count(ia, ib, p.Nq, nk, BN, Cfg::CAUSAL, shift);
+    n_kv[t] = kv_tile_count(ia, ib, nq, nk, BN, Cfg::CAUSAL, shift);
     nmax = n_kv[t] > nmax ? n_kv[t] : nmax;
   }
 
@@ -172,7 +195,7 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
     const uint32_t o_taddr = tmem + lane_off + (uint32_t)(Cfg::O_COL0 + t * D);
     float sl2 = p.sl2;
     if constexpr (Cfg::FP8) sl2 *= __ldg(p.dq) * __ldg(p.dk);
-    const long long vend = vis_end(row, p.Nq, nk, Cfg::CAUSAL, shift);
+    const long long vend = vis_end(row, nq, nk, Cfg::CAUSAL, shift);
     float m_ref = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < nt; ++j) {
@@ -182,7 +205,7 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
       if (!ok) break;
       ptx::tc_fence_after();
       const uint32_t s_taddr = tmem + lane_off + (uint32_t)(si * BN);
-      const bool partial = tile_kind(ia, ib, j, p.Nq, nk, BN, Cfg::CAUSAL, shift) == kTilePartial;
+      const bool partial = tile_kind(ia, ib, j, nq, nk, BN, Cfg::CAUSAL, shift) == kTilePartial;
       const int nvis = (int)(vend - (long long)j * BN);  // visible keys of this tile (masks partial tiles)
       // ---- one read of the whole score row per tile, in two halves: the
       // second half's loads are in flight while the first half's maximum is
@@ -338,13 +361,27 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
     }
     if (ok) {
       ptx::tc_fence_after();
-      const bool store = row < p.Nq;
+      const bool store = row < nq;
       float inv = l > 0.f ? 1.f / l : 0.f;
       if constexpr (Cfg::FP8) inv *= __ldg(p.dv);
-      const float lse = l > 0.f ? (m_ref + log2f(l)) * 0.6931471805599453f : -INFINITY;
-      if (p.o_part == nullptr) {
-        __nv_bfloat16* orow =
-            reinterpret_cast<__nv_bfloat16*>(p.o) + (((long long)b * p.Nq + row) * p.Hq + h) * (long long)D;
+      float lse = l > 0.f ? (m_ref + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      if constexpr (Cfg::RAGGED != 0) {
+        if (l != l) inv = lse = l;  // a row whose scores hold a NaN
+      }
+      // first element of the row in [tokens, Hq, D], and its place in lse
+      long long tok, lse_at;
+      bool final_out;
+      if constexpr (Cfg::RAGGED != 0) {
+        tok = (long long)q_base + row;
+        lse_at = (long long)h * p.rg.Tq + tok;
+        final_out = p.o_part == nullptr || nk_all <= p.kv_chunk;  // (one window only)
+      } else {
+        tok = (long long)b * p.Nq + row;
+        lse_at = ((long long)b * p.Hq + h) * p.Nq + row;
+        final_out = p.o_part == nullptr;
+      }
+      if (final_out) {
+        __nv_bfloat16* orow = reinterpret_cast<__nv_bfloat16*>(p.o) + (tok * p.Hq + h) * (long long)D;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t r[32];
@@ -363,11 +400,18 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
             for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
           }
         }
-        if (store && p.lse != nullptr) p.lse[((long long)b * p.Hq + h) * p.Nq + row] = lse;
+        if (store && p.lse != nullptr) p.lse[lse_at] = lse;
       } else {
         // split-KV partial of window `split`: fp32 O_s and LSE_s
-        const long long zs = (long long)split * p.B + b;
-        float* orow = p.o_part + ((zs * p.Nq + row) * p.Hq + h) * (long long)D;
+        long long prow, plse;
+        if constexpr (Cfg::RAGGED != 0) {
+          prow = plse = ((long long)split * p.rg.Tq + tok) * p.Hq + h;
+        } else {
+          const long long zs = (long long)split * p.B + b;
+          prow = (zs * p.Nq + row) * p.Hq + h;
+          plse = (zs * p.Hq + h) * p.Nq + row;
+        }
+        float* orow = p.o_part + prow * (long long)D;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t r[32];
@@ -384,13 +428,16 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
                               : make_float4(0.f, 0.f, 0.f, 0.f);
           }
         }
-        if (store) p.lse_part[(zs * p.Hq + h) * p.Nq + row] = lse;
+        if (store) p.lse_part[plse] = lse;
       }
     }
   } else if (warp == Cfg::TMA_WARP) {
     // ------------------------------------------------------------ producer
     if constexpr (Cfg::SPLIT_REGS) ptx::setmaxnreg_dec<Cfg::REG_CONTROL>();
-    if (lane == 0) {
+    // (over a paged cache the whole warp runs the loop: lane i fetches the
+    // tile's page i and issues its boxes)
+    constexpr bool PAGED = Cfg::RAGGED == 2;
+    if (PAGED || lane == 0) {
       int k_issued[KST], v_issued[VST];
 #pragma unroll
       for (int s = 0; s < KST; ++s) k_issued[s] = 0;
@@ -401,42 +448,70 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
       for (int t = 0; t < NQT; ++t) {
         q_issued[t] = n_kv[t] > 0;
         if (!q_issued[t]) continue;
+        if (PAGED && lane != 0) continue;
         const uint32_t fb = bar(Cfg::B_QFULL + t);
         ptx::mbar_arrive_expect_tx(fb, Cfg::QT_BYTES);
 #pragma unroll
         for (int c = 0; c < Cfg::NCH; ++c) {
           const uint32_t dst = sbase + Cfg::OFF_Q + t * Cfg::QT_BYTES + c * Cfg::CH_Q;
           if (Cfg::PACK && g > 1)  // box: g heads x BM / g rows of kv head kh
-            ptx::tma_load_5d(dst, &tmQ, fb, c * Cfg::BOXE, 0, kh, (q0 + t * BM) / g, b);
+            ptx::tma_load_5d(dst, &tmQ, fb, c * Cfg::BOXE, 0, kh, q_base + (q0 + t * BM) / g, b);
           else
-            ptx::tma_load_4d(dst, &tmQ, fb, c * Cfg::BOXE, hy, q0 + t * BM, b);
+            ptx::tma_load_4d(dst, &tmQ, fb, c * Cfg::BOXE, hy, q_base + q0 + t * BM, b);
         }
       }
-      for (int j = 0; j < nmax; ++j) {
-        const int ks = j % KST;
-        if (j >= KST && !wait_bar<kRoleProducer>(bar(Cfg::B_KEMPTY + ks), (uint32_t)(((j / KST) - 1) & 1), wc, kSiteKEmpty))
-          break;
-        {
-          const uint32_t fb = bar(Cfg::B_KFULL + ks);
+      auto wait_empty = [&](uint32_t eb, uint32_t parity, uint32_t site) -> bool {
+        if constexpr (PAGED) return wait_bar_warp<kRoleProducer>(eb, parity, wc, site);
+        else return wait_bar<kRoleProducer>(eb, parity, wc, site);
+      };
+      // one operand's key tile: the boxes that make up its BN rows
+      auto load_kv = [&](const CUtensorMap* tm, uint32_t dst, uint32_t fb, int j, int page) {
+        if constexpr (PAGED) {
+          if (lane == 0) ptx::mbar_arrive_expect_tx(fb, Cfg::KV_BYTES);
+          __syncwarp();
+          const int ps = 1 << p.rg.page_shift, rows = ps < BN ? ps : BN;  // rows of a box
+          if (lane < BN / rows) {
+            const int r0 = ps < BN ? 0 : (kv0 + j * BN) & (ps - 1);
+#pragma unroll
+            for (int c = 0; c < Cfg::NCH; ++c)
+              ptx::tma_load_4d(dst + c * Cfg::CH_KV + lane * rows * 128, tm, fb, c * Cfg::BOXE, kh, r0, page);
+          }
+        } else {
           ptx::mbar_arrive_expect_tx(fb, Cfg::KV_BYTES);
 #pragma unroll
           for (int c = 0; c < Cfg::NCH; ++c)
-            ptx::tma_load_4d(sbase + Cfg::OFF_K + ks * Cfg::KV_BYTES + c * Cfg::CH_KV, &tmK, fb, c * Cfg::BOXE,
-                             kh, kv0 + j * BN, b);
+            ptx::tma_load_4d(dst + c * Cfg::CH_KV, tm, fb, c * Cfg::BOXE, kh, k_base + kv0 + j * BN, b);
+        }
+      };
+      // the page that holds this lane's rows of tile j; the index n_pages (a
+      // box outside the map: zeros) behind the sequence and for a bad page
+      auto page_of = [&](int j) -> int {
+        if constexpr (!PAGED) return 0;
+        const int ps = 1 << p.rg.page_shift, rows = ps < BN ? ps : BN;
+        const int key = kv0 + j * BN + lane * rows;
+        if (lane >= BN / rows || j * BN + lane * rows >= nk) return p.rg.n_pages;
+        const int pi = key >> p.rg.page_shift;
+        const int id = pi < p.rg.table_width ? __ldg(p.rg.table + (long long)seq * p.rg.table_width + pi) : -1;
+        if (id >= 0 && id < p.rg.n_pages) return id;
+        atomicOr(p.err, kErrIndex);
+        return p.rg.n_pages;
+      };
+      [[maybe_unused]] int page = page_of(0);
+      for (int j = 0; j < nmax; ++j) {
+        [[maybe_unused]] const int page_next = PAGED && j + 1 < nmax ? page_of(j + 1) : 0;
+        const int ks = j % KST;
+        if (j >= KST && !wait_empty(bar(Cfg::B_KEMPTY + ks), (uint32_t)(((j / KST) - 1) & 1), kSiteKEmpty)) break;
+        {
+          load_kv(&tmK, sbase + Cfg::OFF_K + ks * Cfg::KV_BYTES, bar(Cfg::B_KFULL + ks), j, page);
           ++k_issued[ks];
         }
         const int vs = j % VST;
-        if (j >= VST && !wait_bar<kRoleProducer>(bar(Cfg::B_VEMPTY + vs), (uint32_t)(((j / VST) - 1) & 1), wc, kSiteVEmpty))
-          break;
+        if (j >= VST && !wait_empty(bar(Cfg::B_VEMPTY + vs), (uint32_t)(((j / VST) - 1) & 1), kSiteVEmpty)) break;
         {
-          const uint32_t fb = bar(Cfg::B_VFULL + vs);
-          ptx::mbar_arrive_expect_tx(fb, Cfg::KV_BYTES);
-#pragma unroll
-          for (int c = 0; c < Cfg::NCH; ++c)
-            ptx::tma_load_4d(sbase + Cfg::OFF_V + vs * Cfg::KV_BYTES + c * Cfg::CH_KV, &tmV, fb, c * Cfg::BOXE,
-                             kh, kv0 + j * BN, b);
+          load_kv(&tmV, sbase + Cfg::OFF_V + vs * Cfg::KV_BYTES, bar(Cfg::B_VFULL + vs), j, page);
           ++v_issued[vs];
         }
+        page = page_next;
       }
       // Every issued copy must land before the block may exit (no-op in the
       // normal path, where the consumers have already seen them all).
@@ -503,6 +578,22 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
         if (jj == n_kv[t] - 1) ptx::warp_commit(bar(Cfg::B_OFINAL + t));
         return true;
       };
+      // RAGGED: rows of the V tile behind the last key hold what is not this
+      // sequence's; a masked weight of zero times a NaN there would reach every
+      // row, so they are cleared before the first product reads the tile
+      auto clear_tail = [&](int jj) {
+        const int valid = nk - jj * BN;
+        if (valid >= BN) return;
+        const uint32_t v0 = v_s + (jj % VST) * Cfg::KV_BYTES + (uint32_t)lane * 16u;
+        for (int r = (valid > 0 ? valid : 0) * 128; r < BN * 128; r += 512) {
+          if (r + lane * 16 < BN * 128) {
+#pragma unroll
+            for (int c = 0; c < Cfg::NCH; ++c) ptx::st_shared_v4(v0 + c * Cfg::CH_KV + r, 0u, 0u, 0u, 0u);
+          }
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+      };
       for (int j = 0; ok && j <= nmax; ++j) {
         const bool has_k = j < nmax, has_v = j >= 1;
         if constexpr (SB == 2) {
@@ -522,6 +613,7 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
             ok = wait_bar_warp<kRoleMma>(bar(Cfg::B_VFULL + (j - 1) % VST), (uint32_t)(((j - 1) / VST) & 1),
                                          wc, kSiteVFull);
             if (!ok) break;
+            if constexpr (Cfg::RAGGED != 0) clear_tail(j - 1);
             ptx::tc_fence_after();
 #pragma unroll
             for (int t = 0; t < NQT && ok; ++t)
@@ -540,6 +632,7 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
             ok = wait_bar_warp<kRoleMma>(bar(Cfg::B_VFULL + (j - 1) % VST), (uint32_t)(((j - 1) / VST) & 1),
                                          wc, kSiteVFull);
             if (!ok) break;
+            if constexpr (Cfg::RAGGED != 0) clear_tail(j - 1);
           }
           ptx::tc_fence_after();
 #pragma unroll

@@ -1,0 +1,147 @@
+// ragged_plan.cuh -- the list of work items of an attention over packed
+// sequences: one item per (sequence, block of query rows), longest first.
+//
+// The lengths live on the device, so the host cannot build the list; one block
+// does, ahead of the attention kernel (whose launch overlaps it).  An item's
+// cost is the number of key tiles its last row sees; items are handed out in
+// falling order of cost by a counting sort over kPlanBuckets levels (the order
+// within a level is arbitrary and does not affect any result).
+#pragma once
+#include <cstdint>
+
+#include "attn_common.cuh"
+#include "ptx.cuh"
+#include "tiles.h"
+
+namespace attn {
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanBuckets = 256;
+constexpr int kPlanHead = 8;   // ints in front of the items
+constexpr int kPlanItem = 8;   // ints of an item
+
+struct PlanParams {
+  int* plan;
+  int max_items;
+  int n_seqs, Tq, Tk, max_q, max_kv;
+  const int* cu_q;     // or nullptr: sequence s has the rows [s * max_q, (s + 1) * max_q)
+  const int* cu_k;     // packed keys; nullptr: paged
+  const int* kv_lens;  // paged
+  int rows_per_token;  // packed rows of a token (1 or the group size)
+  int block_rows, bn;
+  bool causal;
+  unsigned int* err;
+};
+
+// A boundary pair of the device clamped to [0, total].
+__device__ __forceinline__ int2 clamped_range(const int* cu, int s, int total, bool& bad) {
+  int a = __ldg(cu + s), b = __ldg(cu + s + 1);
+  if (a < 0 || b < a || b > total) {
+    bad = true;
+    a = a < 0 ? 0 : (a > total ? total : a);
+    b = b < a ? a : (b > total ? total : b);
+  }
+  return make_int2(a, b);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) ragged_plan_kernel(const PlanParams p) {
+  __shared__ int s_hist[kPlanBuckets], s_max, s_count;
+  ptx::grid_dep_launch();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int NW = kPlanThreads / 32;
+  for (int i = tid; i < kPlanBuckets; i += kPlanThreads) s_hist[i] = 0;
+  if (tid == 0) s_max = s_count = 0;
+  __syncthreads();
+  bool bad = false;
+  auto seq = [&](int s, int& q0, int& nq, int& k0, int& nk) {
+    if (p.cu_q != nullptr) {
+      const int2 q = clamped_range(p.cu_q, s, p.Tq, bad);
+      q0 = q.x;
+      nq = q.y - q.x;
+    } else {
+      q0 = s * p.max_q;
+      nq = p.max_q;
+    }
+    if (nq > p.max_q) {
+      bad = true;
+      nq = p.max_q;
+    }
+    if (p.cu_k != nullptr) {
+      const int2 k = clamped_range(p.cu_k, s, p.Tk, bad);
+      k0 = k.x;
+      nk = k.y - k.x;
+    } else {
+      k0 = 0;
+      nk = __ldg(p.kv_lens + s);
+      if (nk < 0 || nk > p.max_kv) {
+        bad = true;
+        nk = nk < 0 ? 0 : p.max_kv;
+      }
+    }
+  };
+  auto blocks_of = [&](int nq) -> int {
+    return (int)(((long long)nq * p.rows_per_token + p.block_rows - 1) / p.block_rows);
+  };
+  auto cost = [&](int qb, int nq, int nk) -> int {  // key tiles of the block's last row
+    const int last = (int)((((long long)(qb + 1) * p.block_rows) + p.rows_per_token - 1) / p.rows_per_token);
+    return (int)((vis_end((last < nq ? last : nq) - 1, nq, nk, p.causal) + p.bn - 1) / p.bn);
+  };
+  // the largest cost: every sequence's last block
+  int mx = 0;
+  for (int s = tid; s < p.n_seqs; s += kPlanThreads) {
+    int q0, nq, k0, nk;
+    seq(s, q0, nq, k0, nk);
+    const int nb = blocks_of(nq);
+    if (nb > 0) {
+      const int c = cost(nb - 1, nq, nk);
+      mx = c > mx ? c : mx;
+    }
+  }
+  atomicMax(&s_max, mx);
+  __syncthreads();
+  const long long top = s_max + 1;
+  auto level = [&](int c) -> int { return kPlanBuckets - 1 - (int)((long long)c * kPlanBuckets / top); };
+  // two passes over all items: count per level, then place
+  for (int s = warp; s < p.n_seqs; s += NW) {
+    int q0, nq, k0, nk;
+    seq(s, q0, nq, k0, nk);
+    const int nb = blocks_of(nq);
+    for (int qb = lane; qb < nb; qb += 32) atomicAdd(&s_hist[level(cost(qb, nq, nk))], 1);
+  }
+  __syncthreads();
+  if (warp == 0) {  // exclusive prefix sums of the levels
+    int base = 0;
+    for (int i = 0; i < kPlanBuckets; i += 32) {
+      const int v = s_hist[i + lane];
+      int x = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      s_hist[i + lane] = base + x - v;
+      base += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) s_count = base;
+  }
+  __syncthreads();
+  for (int s = warp; s < p.n_seqs; s += NW) {
+    int q0, nq, k0, nk;
+    seq(s, q0, nq, k0, nk);
+    const int nb = blocks_of(nq);
+    for (int qb = lane; qb < nb; qb += 32) {
+      const int at = atomicAdd(&s_hist[level(cost(qb, nq, nk))], 1);
+      if (at < p.max_items) {
+        int4* it = reinterpret_cast<int4*>(p.plan + kPlanHead + kPlanItem * at);
+        it[0] = make_int4(s, qb, q0, nq);
+        it[1] = make_int4(k0, nk, 0, 0);
+      } else {
+        bad = true;  // (boundaries that overlap)
+      }
+    }
+  }
+  if (tid == 0) p.plan[0] = s_count < p.max_items ? s_count : p.max_items;
+  if (bad) atomicOr(p.err, kErrIndex);
+}
+
+}  // namespace attn

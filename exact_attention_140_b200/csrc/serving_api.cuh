@@ -1,0 +1,671 @@
+// serving_api.cuh -- host side of the serving operators: argument checks,
+// choice of kernel and of the key windows, launches.  Part of attn_api.cu (it
+// uses that file's device state, map cache and log).
+#pragma once
+
+namespace attn {
+namespace {
+
+bool head_size_ok(int d) { return d == 64 || d == 128 || d == 256; }
+
+// Checks of a cache description; its pointers only where it has pages.
+int check_cache(const attn_kv_cache_t* c) {
+  if (c == nullptr || c->n_pages < 0 || c->Hkv < 1) return ATTN_ERR_INVALID_ARG;
+  if (c->dtype != ATTN_BF16 && c->dtype != ATTN_FP8_E4M3) return ATTN_ERR_INVALID_ARG;
+  if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)) != 0) return ATTN_ERR_INVALID_ARG;
+  if (!head_size_ok(c->d) || c->Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
+  if (c->n_pages == 0) return ATTN_OK;
+  if (c->k_pages == nullptr || c->v_pages == nullptr) return ATTN_ERR_INVALID_ARG;
+  const bool e4m3 = c->dtype == ATTN_FP8_E4M3;
+  if (e4m3 != (c->k_exp != nullptr) || e4m3 != (c->v_exp != nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(c->k_pages) || !aligned16(c->v_pages)) return ATTN_ERR_MISALIGNED;
+  return ATTN_OK;
+}
+int page_shift(const attn_kv_cache_t* c) {
+  int s = 0;
+  while ((1 << s) < c->page_size) ++s;
+  return s;
+}
+
+// A [T, H, d] tensor with a token stride.
+int check_rows(const void* x, int H, int d, long long stride) {
+  if (x == nullptr || stride < (long long)H * d) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(x) || stride % 8 != 0) return ATTN_ERR_MISALIGNED;
+  return ATTN_OK;
+}
+
+int check_rope(const attn_rope_t* r, int d, const long long* positions) {
+  if (r == nullptr || !std::isfinite(r->eps) || r->eps < 0.f || !std::isfinite(r->amplitude)) return ATTN_ERR_INVALID_ARG;
+  if (r->interleaved != 0 && r->interleaved != 1) return ATTN_ERR_INVALID_ARG;
+  if (r->rot_dim < 0 || r->rot_dim > d || r->rot_dim % 16 != 0) return ATTN_ERR_INVALID_ARG;
+  if (r->rot_dim > 0 && (r->freqs == nullptr || positions == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(r->q_weight) || !aligned16(r->k_weight)) return ATTN_ERR_MISALIGNED;
+  if (r->rot_dim > 0 && ((reinterpret_cast<uintptr_t>(r->freqs) | reinterpret_cast<uintptr_t>(positions)) & 7u) != 0)
+    return ATTN_ERR_MISALIGNED;
+  return ATTN_OK;
+}
+
+void fill_rope(HeadRowsParams* p, const attn_rope_t* r, const long long* positions) {
+  p->q_weight = static_cast<const __nv_bfloat16*>(r->q_weight);
+  p->k_weight = static_cast<const __nv_bfloat16*>(r->k_weight);
+  p->eps = r->eps;
+  p->amplitude = r->amplitude;
+  p->freqs = r->freqs;
+  p->rot = r->rot_dim;
+  p->interleaved = r->interleaved != 0;
+  p->positions = positions;
+}
+
+template <int D>
+int launch_head_rows_d(const HeadRowsParams& p, long long T, DeviceState* st, cudaStream_t s) {
+  constexpr int NG = 256 / (D / 8);
+  const int rows = p.Hq + p.Hkv + (p.has_v ? p.Hkv : 0);
+  // four rows per lane group hide the loads' latency in a long grid; a short
+  // one spreads a token's rows over more blocks instead
+  const bool wide = T * ((rows + NG * 4 - 1) / (NG * 4)) >= 4ll * st->num_sms;
+  const unsigned gy = (unsigned)(wide ? (rows + NG * 4 - 1) / (NG * 4) : (rows + NG - 1) / NG);
+  if (gy > 65535u) return ATTN_ERR_UNSUPPORTED;
+  ATTN_LOGF("attn: head_rows_kernel<%d, %d> grid=(%lld,%u) block=256 Hq=%d Hkv=%d rot=%d cache=%s\n", D, wide ? 4 : 1, T,
+            gy, p.Hq, p.Hkv, p.rot, !p.to_cache ? "no" : (p.k_exp != nullptr ? "e4m3" : "bf16"));
+  if (wide)
+    head_rows_kernel<D, 4><<<dim3((unsigned)T, gy), 256, 0, s>>>(p);
+  else
+    head_rows_kernel<D, 1><<<dim3((unsigned)T, gy), 256, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+int launch_head_rows(const HeadRowsParams& p, int d, long long T, DeviceState* st, cudaStream_t s) {
+  if (p.Hq + p.Hkv == 0) return ATTN_OK;
+  switch (d) {
+    case 64: return launch_head_rows_d<64>(p, T, st, s);
+    case 128: return launch_head_rows_d<128>(p, T, st, s);
+    default: return launch_head_rows_d<256>(p, T, st, s);
+  }
+}
+
+template <int D, bool E4M3>
+int launch_kv_read(const KvReadParams& p, cudaStream_t s) {
+  const long long blocks = (p.T + 7) / 8;  // a warp per token
+  if (blocks > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;
+  ATTN_LOGF("attn: kv_read_kernel<%d, %s> grid=(%lld) block=256 T=%lld Hkv=%d\n", D, E4M3 ? "e4m3" : "bf16", blocks, p.T,
+            p.Hkv);
+  kv_read_kernel<D, E4M3><<<(unsigned)blocks, 256, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- paged attention
+// Windows of a paged call.
+struct PagedPlan {
+  int rw, row_tiles, window, n_windows;
+  long long items;  // > 0: tcgen05 kernel over this many listed items at most
+};
+long long ragged_max_items(long long Tq, long long n_seqs, int Hq, int Hkv, int d);
+int ragged_block_rows(int d);
+int ragged_rows_per_token(int Hq, int Hkv);
+long long ragged_plan_bytes(long long items);
+
+PagedPlan paged_plan(const attn_kv_cache_t* c, int Tq, int n_seqs, int max_q, int Hq, int max_kv, int n_splits) {
+  PagedPlan pl = {};
+  const int Hkv = c->Hkv;
+  const long long rows = (long long)max_q * (Hq / Hkv);
+  if (rows > 64 && c->dtype == ATTN_BF16 && c->n_pages > 0) {
+    pl.items = ragged_max_items(Tq, n_seqs, Hq, Hkv, c->d);
+    const int g = ragged_rows_per_token(Hq, Hkv);
+    long long want = n_splits;
+    if (n_splits <= 0) {  // about two blocks per SM, windows of 512 keys at least
+      const long long blocks = ((long long)Tq * g / ragged_block_rows(c->d) + (n_seqs + 1) / 2) * (g > 1 ? Hkv : Hq);
+      want = (2ll * 148 + blocks - 1) / (blocks > 0 ? blocks : 1);
+      const long long cap = max_kv / 512;
+      want = want > cap ? cap : want;
+      want = want < 1 ? 1 : want;
+    }
+    const long long w = (((long long)max_kv + want - 1) / want + 127) / 128 * 128;
+    pl.window = (int)(w < 128 ? 128 : w);
+    pl.n_windows = max_kv > pl.window ? (int)(((long long)max_kv + pl.window - 1) / pl.window) : 1;
+    return pl;
+  }
+  pl.rw = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
+  pl.row_tiles = (int)((rows + 16 * pl.rw - 1) / (16 * pl.rw));
+  long long w;
+  if (n_splits > 0) {
+    w = ((long long)max_kv + n_splits - 1) / n_splits;
+  } else {
+    // enough blocks to fill the GPU a few times over, windows of 128 keys at least
+    const long long units = (long long)n_seqs * Hkv * pl.row_tiles;
+    w = units * max_kv / (8 * 148);
+    w = w < 128 ? 128 : w;
+  }
+  w = (w + 63) / 64 * 64;
+  pl.window = (int)(w < 64 ? 64 : (w > 2048 ? 2048 : w));
+  pl.n_windows = max_kv > pl.window ? (max_kv + pl.window - 1) / pl.window : 1;
+  return pl;
+}
+// Workspace: the item list, then the windows' partial rows and their LSE.
+long long paged_list_bytes(const PagedPlan& pl) { return pl.items > 0 ? ragged_plan_bytes(pl.items) : 0; }
+long long paged_o_bytes(const PagedPlan& pl, long long Tq, long long Hq, long long d) {
+  return (pl.n_windows * Tq * Hq * d * 4 + 255) / 256 * 256;
+}
+long long paged_bytes(const PagedPlan& pl, long long Tq, long long Hq, long long d) {
+  return paged_list_bytes(pl) + (pl.n_windows > 1 ? paged_o_bytes(pl, Tq, Hq, d) + pl.n_windows * Tq * Hq * 4 : 0);
+}
+
+template <class Cfg>
+int launch_paged_cfg(const PagedParams& p, DeviceState* st, cudaStream_t s) {
+  static std::atomic<unsigned> attr_set[kMaxDevices];
+  int rc = set_smem_once(paged_fwd_kernel<Cfg>, (int)Cfg::SMEM, attr_set, st);
+  if (rc != ATTN_OK) return rc;
+  const long long blocks = (long long)p.n_windows * p.row_tiles * p.Hkv * p.n_seqs;
+  if (blocks > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;
+  ATTN_LOGF("attn: paged_fwd_kernel<%d, %s, RW=%d> grid=(%lld) block=128 smem=%u seqs=%d max_q=%d Hq=%d Hkv=%d windows=%d x %d\n",
+            Cfg::D, Cfg::E4M3 ? "e4m3" : "bf16", Cfg::RW, blocks, (unsigned)Cfg::SMEM, p.n_seqs, p.max_q, p.Hq, p.Hkv,
+            p.n_windows, p.window);
+  paged_fwd_kernel<Cfg><<<(unsigned)blocks, 128, Cfg::SMEM, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+template <int D, bool E4M3>
+int launch_paged_rw(const PagedParams& p, int rw, DeviceState* st, cudaStream_t s) {
+  switch (rw) {
+    case 1: return launch_paged_cfg<PagedCfg<D, E4M3, 1>>(p, st, s);
+    case 2: return launch_paged_cfg<PagedCfg<D, E4M3, 2>>(p, st, s);
+    default: return launch_paged_cfg<PagedCfg<D, E4M3, 4>>(p, st, s);
+  }
+}
+template <int D>
+int launch_paged_combine(const PagedParams& p, cudaStream_t s) {
+  const long long blocks = ((long long)p.Tq * p.Hq + 7) / 8;
+  if (blocks > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;
+  // launched while the attention kernel still runs; it waits for that kernel's
+  // results on the device, so only its launch overlaps
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  ATTN_LOGF("attn: paged_combine_kernel<%d> grid=(%lld) block=256 Tq=%d Hq=%d windows=%d\n", D, blocks, p.Tq, p.Hq,
+            p.n_windows);
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D>, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+template <int D>
+int launch_paged(const PagedParams& p, bool e4m3, int rw, DeviceState* st, cudaStream_t s) {
+  const int rc = e4m3 ? launch_paged_rw<D, true>(p, rw, st, s) : launch_paged_rw<D, false>(p, rw, st, s);
+  if (rc != ATTN_OK || p.n_windows == 1) return rc;
+  return launch_paged_combine<D>(p, s);
+}
+
+// ---------------------------------------------------------------- packed sequences on tcgen05
+// The long-range configurations over packed sequences (1) or a paged cache (2);
+// the heads of a group are always stacked where the group divides the tile: a
+// block then covers fewer tokens, which wastes less of a causal block's diagonal
+// and of a short sequence, and a key tile is read once per group.
+template <bool C, int R> using CfgRagD64 = FwdCfg<64, 128, 2, 3, 3, C, false, 0, 1, false, 1, true, false, R>;
+template <bool C, int R> using CfgRagD128 = FwdCfg<128, 128, 2, 2, 2, C, false, 0, 1, false, 1, true, false, R>;
+template <bool C, int R> using CfgRagD256 = FwdCfg<256, 64, 1, 2, 2, C, false, 0, 2, false, 1, true, false, R>;
+
+int ragged_block_rows(int d) { return d == 256 ? 128 : 256; }
+int ragged_rows_per_token(int Hq, int Hkv) { return pack_factor(Hq, Hkv); }
+// Items at most: every sequence may end in a block of one row.
+long long ragged_max_items(long long Tq, long long n_seqs, int Hq, int Hkv, int d) {
+  const long long R = ragged_block_rows(d), n = n_seqs < Tq ? n_seqs : Tq;
+  return (Tq * ragged_rows_per_token(Hq, Hkv) + n * (R - 1)) / R;
+}
+long long ragged_plan_bytes(long long items) { return (4 * (kPlanHead + kPlanItem * items) + 255) / 256 * 256; }
+
+struct RaggedCall {
+  const void *q, *k, *v;
+  void* o;
+  float* lse;
+  int Tq, Tk, n_seqs, max_q, Hq, Hkv, d;
+  const int *cu_q, *cu_k, *kv_lens, *table;
+  int table_width, max_kv;
+  long long q_stride, k_stride, v_stride;
+  const attn_kv_cache_t* cache;  // paged
+  bool causal;
+  float scale;
+  int n_windows, window;
+  float *o_part, *lse_part;
+  int* plan;
+};
+
+template <class Cfg>
+int launch_ragged(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
+  static std::atomic<unsigned> attr_set[kMaxDevices];
+  int rc = set_smem_once(attn_fwd_kernel<Cfg>, (int)Cfg::SMEM_BYTES, attr_set, st);
+  if (rc != ATTN_OK) return rc;
+  const int g = ragged_rows_per_token(c.Hq, c.Hkv);
+  const long long items = ragged_max_items(c.Tq, c.n_seqs, c.Hq, c.Hkv, c.d);
+  const int nh = g > 1 ? c.Hkv : c.Hq;
+  const long long blocks = items * nh * c.n_windows;
+  if (blocks > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;
+  CUtensorMap tq, tk, tv;
+  rc = g > 1 ? encode_packed_groups(&tq, c.q, c.Tq, c.Hq, g, c.d, c.q_stride, Cfg::BM)
+             : encode_packed(&tq, c.q, c.Tq, c.Hq, c.d, c.q_stride, Cfg::BM);
+  if (rc != ATTN_OK) return rc;
+  if (Cfg::RAGGED == 1) {
+    // (no key anywhere: the maps are never used, and a map of no rows cannot be made)
+    if (c.Tk == 0) {
+      tk = tv = tq;
+    } else if (encode_packed(&tk, c.k, c.Tk, c.Hkv, c.d, c.k_stride, Cfg::BN) != ATTN_OK ||
+               encode_packed(&tv, c.v, c.Tk, c.Hkv, c.d, c.v_stride, Cfg::BN) != ATTN_OK) {
+      return ATTN_ERR_CUDA;
+    }
+  } else {
+    const attn_kv_cache_t* ch = c.cache;
+    const int rows = ch->page_size < Cfg::BN ? ch->page_size : Cfg::BN;
+    if (encode_pages(&tk, ch->k_pages, ch->n_pages, ch->page_size, ch->Hkv, ch->d, rows) != ATTN_OK ||
+        encode_pages(&tv, ch->v_pages, ch->n_pages, ch->page_size, ch->Hkv, ch->d, rows) != ATTN_OK)
+      return ATTN_ERR_CUDA;
+  }
+  PlanParams pp;
+  pp.plan = c.plan;
+  pp.max_items = (int)items;
+  pp.n_seqs = c.n_seqs;
+  pp.Tq = c.Tq;
+  pp.Tk = c.Tk;
+  pp.max_q = c.max_q;
+  pp.max_kv = c.max_kv;
+  pp.cu_q = c.cu_q;
+  pp.cu_k = c.cu_k;
+  pp.kv_lens = c.kv_lens;
+  pp.rows_per_token = g;
+  pp.block_rows = Cfg::BM * Cfg::NQT;
+  pp.bn = Cfg::BN;
+  pp.causal = c.causal;
+  pp.err = st->err;
+  ATTN_LOGF("attn: ragged_plan_kernel grid=(1) block=%d seqs=%d items<=%lld\n", kPlanThreads, c.n_seqs, items);
+  ragged_plan_kernel<<<1, kPlanThreads, 0, s>>>(pp);
+  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+
+  FwdParams p = {};
+  p.o = c.o;
+  p.lse = c.lse;
+  p.B = 1;
+  p.Hq = c.Hq;
+  p.Hkv = c.Hkv;
+  p.Nq = c.Tq;
+  p.Nk = c.Tk;
+  p.group = c.Hq / c.Hkv;
+  p.nb = 1;
+  p.nh = nh;
+  p.pack = g;
+  p.sl2 = c.scale * 1.4426950408889634f;
+  p.n_splits = c.n_windows;
+  p.kv_chunk = c.n_windows > 1 ? c.window : 0x7FFFFFFF;
+  p.o_part = c.n_windows > 1 ? c.o_part : nullptr;
+  p.lse_part = c.lse_part;
+  p.err = st->err;
+  p.timeout_ns = timeout_ns();
+  // heads whose keys and values fit about 48 MB of L2 run together, as causal attn_fwd launches
+  const long long kv_head = 4ll * c.Tk * c.d / (g > 1 ? 1 : p.group);
+  long long band = (48ll << 20) / (kv_head > 0 ? kv_head : 1);
+  p.band = (int)(band < 1 ? 1 : (band > nh ? nh : band));
+  p.rg.plan = c.plan;
+  p.rg.max_items = (int)items;
+  p.rg.Tq = c.Tq;
+  p.rg.table = c.table;
+  p.rg.table_width = c.table_width;
+  p.rg.page_shift = c.cache != nullptr ? page_shift(c.cache) : 0;
+  p.rg.n_pages = c.cache != nullptr ? c.cache->n_pages : 0;
+  const dim3 grid((unsigned)blocks);
+  if (log_on()) {
+    char extra[96];
+    std::snprintf(extra, sizeof extra, " packed sequences%s windows=%d x %d pack=%d band=%d",
+                  Cfg::RAGGED == 2 ? " (paged)" : "", c.n_windows, c.window, g, p.band);
+    log_launch<Cfg>("attn_fwd_kernel", grid, c.n_seqs, c.Hq, c.Hkv, c.Tq, c.Tk, extra);
+  }
+  cudaLaunchAttribute at;  // the launch overlaps the plan kernel, which the kernel waits for
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(Cfg::NTHREADS);
+  cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_fwd_kernel<Cfg>, tq, tk, tv, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+template <int R>
+int launch_ragged_d(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
+  switch (c.d) {
+    case 64: return c.causal ? launch_ragged<CfgRagD64<true, R>>(c, st, s) : launch_ragged<CfgRagD64<false, R>>(c, st, s);
+    case 128:
+      return c.causal ? launch_ragged<CfgRagD128<true, R>>(c, st, s) : launch_ragged<CfgRagD128<false, R>>(c, st, s);
+    default:
+      return c.causal ? launch_ragged<CfgRagD256<true, R>>(c, st, s) : launch_ragged<CfgRagD256<false, R>>(c, st, s);
+  }
+}
+
+int check_paged_sizes(const attn_kv_cache_t* c, int Tq, int n_seqs, int max_q, int Hq, int max_kv) {
+  int rc = check_cache(c);
+  if (rc != ATTN_OK) return rc;
+  if (Tq < 0 || n_seqs < 0 || Hq < 0 || max_kv < 0 || Hq % c->Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  if (Tq == 0 || n_seqs == 0 || Hq == 0) return -1;  // nothing to compute
+  if (max_q < 1 || max_q > Tq) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+}  // namespace
+}  // namespace attn
+
+extern "C" {
+
+int attn_rope_freqs(double* freqs, int rot_dim, double base, int kind, double factor, double trained_len,
+                    double fast_turns, double slow_turns, float* amplitude) {
+  if (freqs == nullptr || rot_dim < 2 || rot_dim > 65536 || rot_dim % 2 != 0) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(base) || !(base > 1.0) || !std::isfinite(factor) || !(factor >= 1.0)) return ATTN_ERR_INVALID_ARG;
+  if (kind < ATTN_ROPE_PLAIN || kind > ATTN_ROPE_BANDS) return ATTN_ERR_INVALID_ARG;
+  if (kind == ATTN_ROPE_NTK && rot_dim == 2 && factor > 1.0) return ATTN_ERR_INVALID_ARG;  // one pair: no slowest to stretch
+  double low = 0.0, high = 0.0;  // BANDS: the pair indexes between which the frequencies are blended
+  const double two_pi = 6.283185307179586476925;
+  if (kind == ATTN_ROPE_BANDS) {
+    if (!std::isfinite(trained_len) || !(trained_len > 0.0) || !std::isfinite(fast_turns) || !(slow_turns > 0.0) ||
+        !(fast_turns > slow_turns))
+      return ATTN_ERR_INVALID_ARG;
+    // pair i turns trained_len * base^(-2i / rot_dim) / 2 pi times
+    auto index_of = [&](double turns) {
+      return rot_dim * std::log(trained_len / (turns * two_pi)) / (2.0 * std::log(base));
+    };
+    low = std::floor(index_of(fast_turns));
+    high = std::ceil(index_of(slow_turns));
+    low = low < 0.0 ? 0.0 : low;
+    high = high > rot_dim / 2 - 1 ? rot_dim / 2 - 1 : high;
+    if (high <= low) high = low + 1e-3;
+  }
+  const double b = kind == ATTN_ROPE_NTK && factor > 1.0 ? base * std::pow(factor, rot_dim / (rot_dim - 2.0)) : base;
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    const double f = std::pow(b, -2.0 * i / rot_dim);
+    if (kind == ATTN_ROPE_LINEAR) {
+      freqs[i] = f / factor;
+    } else if (kind == ATTN_ROPE_BANDS) {
+      double slow = (i - low) / (high - low);  // share of the stretched frequency
+      slow = slow < 0.0 ? 0.0 : (slow > 1.0 ? 1.0 : slow);
+      freqs[i] = f - (f - f / factor) * slow;
+    } else {
+      freqs[i] = f;
+    }
+  }
+  if (amplitude != nullptr) *amplitude = kind == ATTN_ROPE_BANDS ? (float)(1.0 + 0.1 * std::log(factor)) : 1.f;
+  return ATTN_OK;
+}
+
+int attn_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, long long T, int Hq, int Hkv, int d,
+                      long long q_stride, long long k_stride, long long q_out_stride, long long k_out_stride,
+                      const long long* positions, const attn_rope_t* rope, void* stream) {
+  if (T < 0 || Hq < 0 || Hkv < 0) return ATTN_ERR_INVALID_ARG;
+  if (!head_size_ok(d) || T > 0x7FFFFFFFll || Hq > 65535 || Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
+  int rc = check_rope(rope, d, positions);
+  if (rc != ATTN_OK) return rc;
+  if (T == 0 || (Hq == 0 && Hkv == 0)) return ATTN_OK;
+  if (Hq > 0 && ((rc = check_rows(q, Hq, d, q_stride)) != ATTN_OK || (rc = check_rows(q_out, Hq, d, q_out_stride)) != ATTN_OK))
+    return rc;
+  if (Hkv > 0 &&
+      ((rc = check_rows(k, Hkv, d, k_stride)) != ATTN_OK || (rc = check_rows(k_out, Hkv, d, k_out_stride)) != ATTN_OK))
+    return rc;
+  int dev = 0;
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&dev, &st)) != ATTN_OK) return rc;
+  HeadRowsParams p = {};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.q_out_stride = q_out_stride;
+  p.k_out_stride = k_out_stride;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  fill_rope(&p, rope, positions);
+  p.err = st->err;
+  return launch_head_rows(p, d, T, st, static_cast<cudaStream_t>(stream));
+}
+
+int attn_kv_write(const attn_kv_cache_t* cache, const void* k, const void* v, long long T, long long k_stride,
+                  long long v_stride, const long long* slots, const attn_rope_t* rope, const long long* positions,
+                  const void* q, void* q_out, int Hq, long long q_stride, long long q_out_stride, void* stream) {
+  int rc = check_cache(cache);
+  if (rc != ATTN_OK) return rc;
+  if (T < 0 || Hq < 0) return ATTN_ERR_INVALID_ARG;
+  if (T > 0x7FFFFFFFll || Hq > 65535) return ATTN_ERR_UNSUPPORTED;
+  const int d = cache->d, Hkv = cache->Hkv;
+  if (rope != nullptr && (rc = check_rope(rope, d, positions)) != ATTN_OK) return rc;
+  if (rope == nullptr && Hq > 0) return ATTN_ERR_INVALID_ARG;  // queries only take part in the norm and rotation
+  if (T == 0) return ATTN_OK;
+  if ((rc = check_rows(k, Hkv, d, k_stride)) != ATTN_OK || (rc = check_rows(v, Hkv, d, v_stride)) != ATTN_OK) return rc;
+  if (Hq > 0 && ((rc = check_rows(q, Hq, d, q_stride)) != ATTN_OK || (rc = check_rows(q_out, Hq, d, q_out_stride)) != ATTN_OK))
+    return rc;
+  if (slots == nullptr) return ATTN_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(slots) & 7u) != 0) return ATTN_ERR_MISALIGNED;
+  int dev = 0;
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&dev, &st)) != ATTN_OK) return rc;
+  HeadRowsParams p = {};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out_stride = q_out_stride;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.has_v = true;
+  p.to_cache = true;
+  p.slots = slots;
+  p.n_slots = (long long)cache->n_pages * cache->page_size;
+  p.k_pages = cache->k_pages;
+  p.v_pages = cache->v_pages;
+  p.k_exp = cache->k_exp;
+  p.v_exp = cache->v_exp;
+  if (rope != nullptr) fill_rope(&p, rope, positions);
+  p.err = st->err;
+  return launch_head_rows(p, d, T, st, static_cast<cudaStream_t>(stream));
+}
+
+int attn_kv_read(const attn_kv_cache_t* cache, const int* table, int table_width, const int* cu, int n_seqs, void* k,
+                 void* v, long long T, void* stream) {
+  int rc = check_cache(cache);
+  if (rc != ATTN_OK) return rc;
+  if (T < 0 || n_seqs < 0 || table_width < 0) return ATTN_ERR_INVALID_ARG;
+  if (T == 0 || n_seqs == 0) return ATTN_OK;
+  if (T > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;
+  if (cu == nullptr || k == nullptr || v == nullptr || (table_width > 0 && table == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) ||
+      ((reinterpret_cast<uintptr_t>(cu) | reinterpret_cast<uintptr_t>(table)) & 3u) != 0)
+    return ATTN_ERR_MISALIGNED;
+  int dev = 0;
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&dev, &st)) != ATTN_OK) return rc;
+  KvReadParams p;
+  p.k_pages = cache->k_pages;
+  p.v_pages = cache->v_pages;
+  p.k_exp = cache->k_exp;
+  p.v_exp = cache->v_exp;
+  p.n_pages = cache->n_pages;
+  p.page_shift = page_shift(cache);
+  p.Hkv = cache->Hkv;
+  p.n_seqs = n_seqs;
+  p.table_width = table_width;
+  p.table = table;
+  p.cu = cu;
+  p.k = static_cast<__nv_bfloat16*>(k);
+  p.v = static_cast<__nv_bfloat16*>(v);
+  p.T = T;
+  p.err = st->err;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool e4m3 = cache->dtype == ATTN_FP8_E4M3;
+  switch (cache->d) {
+    case 64: return e4m3 ? launch_kv_read<64, true>(p, s) : launch_kv_read<64, false>(p, s);
+    case 128: return e4m3 ? launch_kv_read<128, true>(p, s) : launch_kv_read<128, false>(p, s);
+    default: return e4m3 ? launch_kv_read<256, true>(p, s) : launch_kv_read<256, false>(p, s);
+  }
+}
+
+long long attn_fwd_varlen_workspace_bytes(int Tq, int n_seqs, int Hq, int Hkv, int d) {
+  if (Tq < 0 || n_seqs < 0 || Hq < 0 || Hkv < 1 || Hq % Hkv != 0 || !head_size_ok(d)) return -1;
+  if (Tq == 0 || n_seqs == 0 || Hq == 0) return 0;
+  return ragged_plan_bytes(ragged_max_items(Tq, n_seqs, Hq, Hkv, d));
+}
+
+int attn_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse, int Tq, int Tk, int n_seqs,
+                    const int* cu_q, const int* cu_k, int Hq, int Hkv, int d, long long q_stride, long long k_stride,
+                    long long v_stride, int causal, float scale, void* workspace, long long workspace_bytes,
+                    void* stream) {
+  if (Tq < 0 || Tk < 0 || n_seqs < 0 || Hq < 0 || Hkv < 0) return ATTN_ERR_INVALID_ARG;
+  if ((causal != 0 && causal != 1) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  if (Tq == 0 || n_seqs == 0 || Hq == 0) return ATTN_OK;
+  if (Hkv == 0 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  if (!head_size_ok(d) || Hq > 65535) return ATTN_ERR_UNSUPPORTED;
+  if (cu_q == nullptr || cu_k == nullptr || o == nullptr) return ATTN_ERR_INVALID_ARG;
+  int rc;
+  if ((rc = check_rows(q, Hq, d, q_stride)) != ATTN_OK) return rc;
+  if (Tk > 0 && ((rc = check_rows(k, Hkv, d, k_stride)) != ATTN_OK || (rc = check_rows(v, Hkv, d, v_stride)) != ATTN_OK))
+    return rc;
+  if (!aligned16(o) || ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(cu_q) |
+                         reinterpret_cast<uintptr_t>(cu_k)) & 3u) != 0)
+    return ATTN_ERR_MISALIGNED;
+  if (workspace == nullptr || workspace_bytes < attn_fwd_varlen_workspace_bytes(Tq, n_seqs, Hq, Hkv, d))
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
+  int dev = 0;
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&dev, &st)) != ATTN_OK) return rc;
+  RaggedCall c = {};
+  c.q = q;
+  c.k = k;
+  c.v = v;
+  c.o = o;
+  c.lse = lse;
+  c.Tq = Tq;
+  c.Tk = Tk;
+  c.n_seqs = n_seqs;
+  c.max_q = Tq;
+  c.Hq = Hq;
+  c.Hkv = Hkv;
+  c.d = d;
+  c.cu_q = cu_q;
+  c.cu_k = cu_k;
+  c.q_stride = q_stride;
+  c.k_stride = k_stride;
+  c.v_stride = v_stride;
+  c.causal = causal != 0;
+  c.scale = scale;
+  c.n_windows = 1;
+  c.plan = static_cast<int*>(workspace);
+  return launch_ragged_d<1>(c, st, static_cast<cudaStream_t>(stream));
+}
+
+long long attn_fwd_paged_workspace_bytes(const attn_kv_cache_t* cache, int Tq, int n_seqs, int max_q, int Hq, int max_kv,
+                                         int n_splits) {
+  const int rc = check_paged_sizes(cache, Tq, n_seqs, max_q, Hq, max_kv);
+  if (rc == -1) return 0;
+  if (rc != ATTN_OK) return -1;
+  const PagedPlan pl = paged_plan(cache, Tq, n_seqs, max_q, Hq, max_kv, n_splits);
+  return paged_bytes(pl, Tq, Hq, cache->d);
+}
+
+int attn_fwd_paged(const void* q, const attn_kv_cache_t* cache, void* o, float* lse, int Tq, int n_seqs, int max_q,
+                   const int* cu_q, const int* table, int table_width, const int* kv_lens, int max_kv, int Hq,
+                   long long q_stride, int causal, float scale, int n_splits, void* workspace,
+                   long long workspace_bytes, void* stream) {
+  int rc = check_paged_sizes(cache, Tq, n_seqs, max_q, Hq, max_kv);
+  if (rc > 0) return rc;
+  if ((causal != 0 && causal != 1) || !std::isfinite(scale) || table_width < 0) return ATTN_ERR_INVALID_ARG;
+  if (rc == -1) return ATTN_OK;
+  const int d = cache->d;
+  if ((long long)table_width * cache->page_size < max_kv) return ATTN_ERR_INVALID_ARG;
+  if (cu_q == nullptr && (long long)n_seqs * max_q != Tq) return ATTN_ERR_INVALID_ARG;
+  if (kv_lens == nullptr || o == nullptr || (max_kv > 0 && table == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if ((rc = check_rows(q, Hq, d, q_stride)) != ATTN_OK) return rc;
+  if (!aligned16(o) || ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(cu_q) |
+                         reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(kv_lens)) & 3u) != 0)
+    return ATTN_ERR_MISALIGNED;
+  const PagedPlan pl = paged_plan(cache, Tq, n_seqs, max_q, Hq, max_kv, n_splits);
+  const long long need = paged_bytes(pl, Tq, Hq, d);
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
+  }
+  int dev = 0;
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&dev, &st)) != ATTN_OK) return rc;
+  PagedParams p;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_stride = q_stride;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.Tq = Tq;
+  p.n_seqs = n_seqs;
+  p.max_q = max_q;
+  p.Hq = Hq;
+  p.Hkv = cache->Hkv;
+  p.group = Hq / cache->Hkv;
+  p.cu_q = cu_q;
+  p.table = table;
+  p.kv_lens = kv_lens;
+  p.table_width = table_width;
+  p.max_kv = max_kv;
+  p.k_pages = cache->k_pages;
+  p.v_pages = cache->v_pages;
+  p.k_exp = cache->k_exp;
+  p.v_exp = cache->v_exp;
+  p.n_pages = cache->n_pages;
+  p.page_shift = page_shift(cache);
+  p.causal = causal;
+  p.sl2 = scale * 1.4426950408889634f;
+  p.n_windows = pl.n_windows;
+  p.window = pl.window;
+  p.row_tiles = pl.row_tiles;
+  char* parts = static_cast<char*>(workspace) + paged_list_bytes(pl);
+  p.o_part = pl.n_windows > 1 ? reinterpret_cast<float*>(parts) : nullptr;
+  p.lse_part = pl.n_windows > 1 ? reinterpret_cast<float*>(parts + paged_o_bytes(pl, Tq, Hq, d)) : nullptr;
+  p.err = st->err;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (pl.items > 0) {
+    RaggedCall c = {};
+    c.q = q;
+    c.o = o;
+    c.lse = lse;
+    c.Tq = Tq;
+    const long long cached = (long long)cache->n_pages * cache->page_size, reach = (long long)n_seqs * max_kv;
+    c.Tk = (int)std::min<long long>(std::min(cached, reach), 0x7FFFFFFF);  // (for the L2 bands only)
+    c.n_seqs = n_seqs;
+    c.max_q = max_q;
+    c.Hq = Hq;
+    c.Hkv = cache->Hkv;
+    c.d = d;
+    c.cu_q = cu_q;
+    c.kv_lens = kv_lens;
+    c.table = table;
+    c.table_width = table_width;
+    c.max_kv = max_kv;
+    c.q_stride = q_stride;
+    c.cache = cache;
+    c.causal = causal != 0;
+    c.scale = scale;
+    c.n_windows = pl.n_windows;
+    c.window = pl.window;
+    c.o_part = p.o_part;
+    c.lse_part = p.lse_part;
+    c.plan = static_cast<int*>(workspace);
+    rc = launch_ragged_d<2>(c, st, s);
+    if (rc != ATTN_OK || pl.n_windows == 1) return rc;
+    switch (d) {
+      case 64: return launch_paged_combine<64>(p, s);
+      case 128: return launch_paged_combine<128>(p, s);
+      default: return launch_paged_combine<256>(p, s);
+    }
+  }
+  const bool e4m3 = cache->dtype == ATTN_FP8_E4M3;
+  switch (d) {
+    case 64: return launch_paged<64>(p, e4m3, pl.rw, st, s);
+    case 128: return launch_paged<128>(p, e4m3, pl.rw, st, s);
+    default: return launch_paged<256>(p, e4m3, pl.rw, st, s);
+  }
+}
+
+}  // extern "C"

@@ -63,7 +63,8 @@ typedef enum {
     ATTN_ERR_UNSUPPORTED = 2,    /* head size or dtype not built, or not an sm_100 device */
     ATTN_ERR_MISALIGNED = 3,     /* a tensor pointer is not 16-byte aligned */
     ATTN_ERR_CUDA = 4,           /* a CUDA runtime/driver call failed */
-    ATTN_ERR_DEVICE_TIMEOUT = 5  /* a device-side wait ran out (see attn_get_last_device_error) */
+    ATTN_ERR_DEVICE_TIMEOUT = 5, /* a device-side wait ran out (see attn_get_last_device_error) */
+    ATTN_ERR_DEVICE_INDEX = 6    /* a kernel met an index outside its array (see attn_get_last_device_error) */
 } attn_status_t;
 
 typedef enum {
@@ -227,10 +228,13 @@ int attn_hadamard_quant_fp8_noalloc(const void *x, void *x8, float *descale, lon
 /*
  * attn_get_last_device_error -- synchronises `stream`, then reads and clears
  * the device error word of the current device.  Returns ATTN_OK,
- * ATTN_ERR_DEVICE_TIMEOUT (a bounded wait ran out inside a kernel) or
+ * ATTN_ERR_DEVICE_TIMEOUT (a bounded wait ran out inside a kernel),
+ * ATTN_ERR_DEVICE_INDEX (a page, slot or sequence boundary that a kernel read
+ * from device memory was outside its array; the kernel did not follow it) or
  * ATTN_ERR_CUDA (the synchronisation itself failed).  If `detail` is not
  * NULL it receives the raw word: bit 0 timeout, bits 8..15 the wait site,
- * bits 16..31 the low bits of the block index.
+ * bits 16..31 the low bits of the block index; bit 1 an index outside its
+ * array.
  */
 int attn_get_last_device_error(void *stream, unsigned int *detail);
 
@@ -326,6 +330,196 @@ int attn_tile_kind_window(int row0, int row1, int kt, int Nq, int Nk, int shift,
  * any other way returns ATTN_ERR_INVALID_ARG.  a and b must not overlap d.
  */
 int attn_gemm_add(const void *a, const void *b, const void *c, void *d, int M, int N, int K, void *stream);
+
+/*
+ * ------------------------------------------------------------------ serving
+ * The operators around the attention of a serving program: norms and position
+ * rotation of queries and keys, a paged key/value cache, and attention over
+ * packed prompts and over the cache.  The pages stop at the attention itself
+ * (page "FlashAttention (SV)"); these keep its formula and its head grouping.
+ *
+ * Packed sequences: the tokens of n sequences stand one after another in one
+ * tensor [T, H, d], and cu (DEVICE int32, n + 1 entries, non-decreasing, cu[0]
+ * >= 0) gives the boundaries: sequence s has the rows [cu[s], cu[s + 1]).
+ * Sequences may be empty.  Rows outside every sequence (a padded batch) are
+ * neither read for a result nor written.
+ * Token strides: the distance between tokens, in elements, so that a tensor
+ * may be a slice of a fused projection's output.  A multiple of 8 and at least
+ * H * d; the heads of a token are contiguous.
+ * Indices read from device memory (boundaries, lengths, pages, slots) cannot
+ * be checked by the host.  A kernel that meets one outside its array does not
+ * follow it: a boundary is clamped to the tensor, a page reads as zeros, a slot is
+ * skipped, and the device error word is set (ATTN_ERR_DEVICE_INDEX from
+ * attn_get_last_device_error).
+ */
+
+/*
+ * A paged key/value cache: pages of page_size tokens; the tokens of a sequence
+ * lie in the pages that its row of a page table names, in order.  A token's
+ * slot is page * page_size + (position in the page).
+ *   k_pages, v_pages  DEVICE [n_pages, page_size, Hkv, d], contiguous, 16-byte
+ *                     aligned; bf16 (dtype ATTN_BF16) or e4m3 (ATTN_FP8_E4M3)
+ *   k_exp, v_exp      e4m3: DEVICE [n_pages, page_size, Hkv] bytes, the scale
+ *                     of each token and head as a power of two:
+ *                     value = code * 2^(exp - 127), exp 1 .. 254; exp 255
+ *                     makes the row NaN.  The codes 0x7F and 0xFF are not
+ *                     used outside such rows.  bf16: NULL
+ *   n_pages           >= 0;  page_size a power of two, 16 .. 4096
+ *   Hkv, d            key/value heads (1 .. 65535); d 64, 128 or 256
+ * The scale is a power of two, so a cached value is exact in bf16 (but for what
+ * leaves bf16's range: a row near its largest value may round to an infinity)
+ * and attention over the cache is attention over exactly the values that
+ * attn_kv_read gives back.
+ */
+typedef struct {
+    void *k_pages, *v_pages;
+    unsigned char *k_exp, *v_exp;
+    int n_pages, page_size, Hkv, d, dtype;
+} attn_kv_cache_t;
+
+/*
+ * Norm and rotation of queries and keys.
+ *   q_weight, k_weight  DEVICE bf16 [d] or NULL: with a weight w each head row
+ *                       x becomes x / sqrt(mean(x^2) + eps) * w
+ *   eps                 finite, >= 0
+ *   freqs               DEVICE fp64 [rot_dim / 2]: the angle per position, in
+ *                       radians, of each pair (attn_rope_freqs); NULL only if
+ *                       rot_dim is 0
+ *   rot_dim             elements of each head that are rotated: a multiple of
+ *                       16, 0 .. d; the elements behind them are left as they are
+ *   interleaved         0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1)
+ *   amplitude           finite; multiplies the cosines and sines
+ * A pair (a, b) at position p becomes (a c - b s, b c + a s) with
+ * c, s = amplitude * (cos, sin)(p * freq); the angle is reduced in fp64, so far
+ * positions keep their accuracy.  Norm and rotation are computed in fp32 and
+ * rounded once.
+ */
+typedef struct {
+    const void *q_weight, *k_weight;
+    const double *freqs;
+    float eps, amplitude;
+    int rot_dim, interleaved;
+} attn_rope_t;
+
+/*
+ * attn_rope_freqs -- the frequencies of attn_rope_t, for a context longer than
+ * the trained one too.  Host only.  freqs (HOST, rot_dim / 2 doubles) gets
+ * base^(-2i / rot_dim), scaled by `kind`:
+ *   ATTN_ROPE_PLAIN   as they are
+ *   ATTN_ROPE_LINEAR  divided by factor (positions interpolated)
+ *   ATTN_ROPE_NTK     with the base raised to base * factor^(rot_dim / (rot_dim - 2)),
+ *                     so the slowest pair is stretched by factor and the
+ *                     fastest not at all
+ *   ATTN_ROPE_BANDS   by wavelength against the trained length: a pair that
+ *                     turns at least fast_turns times in trained_len tokens
+ *                     keeps its frequency, one that turns at most slow_turns
+ *                     times is divided by factor, those between are blended
+ *                     linearly in the pair index; *amplitude is then
+ *                     1 + 0.1 ln(factor)
+ * *amplitude (may be NULL) is 1 for the other kinds.  rot_dim even, 2 .. 65536;
+ * base > 1; factor >= 1; trained_len > 0 and fast_turns > slow_turns > 0 for
+ * ATTN_ROPE_BANDS (unused otherwise).  Returns ATTN_OK or ATTN_ERR_INVALID_ARG.
+ */
+typedef enum { ATTN_ROPE_PLAIN = 0, ATTN_ROPE_LINEAR = 1, ATTN_ROPE_NTK = 2, ATTN_ROPE_BANDS = 3 } attn_rope_kind_t;
+int attn_rope_freqs(double *freqs, int rot_dim, double base, int kind, double factor, double trained_len,
+                    double fast_turns, double slow_turns, float *amplitude);
+
+/*
+ * attn_qk_norm_rope -- norm and rotation of the query and key heads of T
+ * tokens in one pass.
+ *   q, q_out   DEVICE bf16 [T, Hq, d] with token strides q_stride, q_out_stride
+ *   k, k_out   DEVICE bf16 [T, Hkv, d] with token strides k_stride, k_out_stride
+ *              (Hq or Hkv may be 0: that side is left out, its pointers unused)
+ *   positions  DEVICE int64 [T]; any value; NULL only if rot_dim is 0
+ *   rope       see attn_rope_t (the struct is read during the call only)
+ * q_out may be q itself (same stride), and k_out k; any other overlap of an
+ * output is undefined.  T up to 2^31 - 1.
+ */
+int attn_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out, long long T, int Hq, int Hkv, int d,
+                      long long q_stride, long long k_stride, long long q_out_stride, long long k_out_stride,
+                      const long long *positions, const attn_rope_t *rope, void *stream);
+
+/*
+ * attn_kv_write -- writes the keys and values of T tokens into the cache, and
+ * on request norms and rotates the keys and the same tokens' queries on the way
+ * (one pass where attn_qk_norm_rope and a write would be two).
+ *   k, v       DEVICE bf16 [T, Hkv, d] with token strides k_stride, v_stride
+ *   slots      DEVICE int64 [T]: where each token goes; a negative slot skips
+ *              the token's key and value (padding).  Two tokens of one call
+ *              must not share a slot: what it holds then is undefined.
+ *   rope       NULL: keys are written as they are.  Otherwise keys get
+ *              rope->k_weight's norm and the rotation
+ *   positions  DEVICE int64 [T]; needed if rope->rot_dim > 0
+ *   q, q_out   with rope: DEVICE bf16 [T, Hq, d] as in attn_qk_norm_rope, or
+ *              NULL with Hq = 0 (queries of skipped tokens are computed too)
+ * e4m3 cache: a row of amax a gets the smallest power 2^e with a <= 448 * 2^e
+ * (at least 2^-118; 1 for a row of zeros) and the codes E4M3(x * 2^-e), round
+ * to nearest even; a rotated key is quantised from its fp32 value.  A row that
+ * holds a NaN or an infinity gets exp 255 and reads as NaN.
+ */
+int attn_kv_write(const attn_kv_cache_t *cache, const void *k, const void *v, long long T, long long k_stride,
+                  long long v_stride, const long long *slots, const attn_rope_t *rope, const long long *positions,
+                  const void *q, void *q_out, int Hq, long long q_stride, long long q_out_stride, void *stream);
+
+/*
+ * attn_kv_read -- reads sequences back out of the cache, as packed bf16 rows.
+ *   table      DEVICE int32 [n_seqs, table_width]: row s holds the pages of
+ *              sequence s (entries behind its last page are not read)
+ *   cu         DEVICE int32 [n_seqs + 1]: output rows of each sequence; its
+ *              length is the number of cached tokens that are read
+ *   k, v       DEVICE bf16 [T, Hkv, d] outputs, contiguous
+ */
+int attn_kv_read(const attn_kv_cache_t *cache, const int *table, int table_width, const int *cu, int n_seqs,
+                 void *k, void *v, long long T, void *stream);
+
+/*
+ * attn_fwd_varlen -- attention over packed sequences: attn_fwd's operation on
+ * each sequence by itself (same causal rule: bottom-right aligned within the
+ * sequence; a row that sees no key gets O = 0, LSE = -inf).
+ *   q          DEVICE bf16 [Tq, Hq, d], token stride q_stride; k, v [Tk, Hkv, d],
+ *              strides k_stride, v_stride; d 64, 128 or 256
+ *   o          DEVICE bf16 [Tq, Hq, d] contiguous; lse DEVICE fp32 [Hq, Tq] or NULL
+ *   cu_q, cu_k boundaries of the n_seqs sequences in q and in k, v (may be the
+ *              same array); read on the device only, so a call can be captured
+ *              in a graph and replayed with other lengths
+ *   workspace  DEVICE scratch, 16-byte aligned, of at least
+ *              attn_fwd_varlen_workspace_bytes(Tq, n_seqs, Hq, Hkv, d) bytes, owned by
+ *              the caller; calls that may overlap on the GPU need their own
+ * What one sequence holds never reaches another's rows, not even NaN.  Within a
+ * sequence keys and values must be finite where a causal mask hides them (a
+ * hidden NaN or infinity may reach rows of the same 128-row tile).
+ */
+long long attn_fwd_varlen_workspace_bytes(int Tq, int n_seqs, int Hq, int Hkv, int d);
+int attn_fwd_varlen(const void *q, const void *k, const void *v, void *o, float *lse, int Tq, int Tk, int n_seqs,
+                    const int *cu_q, const int *cu_k, int Hq, int Hkv, int d, long long q_stride, long long k_stride,
+                    long long v_stride, int causal, float scale, void *workspace, long long workspace_bytes,
+                    void *stream);
+
+/*
+ * attn_fwd_paged -- attention of new tokens over the paged cache, which holds
+ * them already (attn_kv_write first): one token per sequence (decoding), or a
+ * chunk of a prompt.
+ *   q          DEVICE bf16 [Tq, Hq, d], token stride q_stride; o, lse as attn_fwd_varlen
+ *   cu_q       boundaries of the sequences' new tokens, or NULL when every
+ *              sequence has max_q of them (then Tq = n_seqs * max_q)
+ *   max_q      an upper bound of a sequence's new tokens, 1 .. Tq; a longer
+ *              sequence is an index outside its array: its last rows are not computed
+ *   table      DEVICE int32 [n_seqs, table_width], as attn_kv_read
+ *   kv_lens    DEVICE int32 [n_seqs]: cached tokens of each sequence, the new
+ *              ones among them; row i of n_new sees key j iff
+ *              j <= i + kv_len - n_new (causal = 1), or every key (causal = 0)
+ *   max_kv     an upper bound of kv_lens, 0 .. table_width * page_size; only
+ *              steers how the work is split, but keys behind it are not read
+ *   n_splits   key windows per sequence, <= 0: chosen from the sizes
+ *   workspace  as attn_fwd_varlen, attn_fwd_paged_workspace_bytes(...) bytes
+ * The cache's memory behind a sequence's last token may hold anything, NaN too.
+ */
+long long attn_fwd_paged_workspace_bytes(const attn_kv_cache_t *cache, int Tq, int n_seqs, int max_q, int Hq,
+                                         int max_kv, int n_splits);
+int attn_fwd_paged(const void *q, const attn_kv_cache_t *cache, void *o, float *lse, int Tq, int n_seqs, int max_q,
+                   const int *cu_q, const int *table, int table_width, const int *kv_lens, int max_kv, int Hq,
+                   long long q_stride, int causal, float scale, int n_splits, void *workspace,
+                   long long workspace_bytes, void *stream);
 
 /*
  * Which kernel attn_fwd / attn_fwd_fp8 launch for a key range of Nk keys at

@@ -1,0 +1,334 @@
+"""Attention over packed sequences and over the paged cache on the GPU, against the 64-bit form."""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+def setup():
+    import torch
+
+    import exact_attention_140_b200 as ea
+    import serving_util as su
+    return torch, ea, su
+
+
+def rand(torch, *shape, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(*shape, device="cuda", generator=g).to(torch.bfloat16)
+
+
+VARLEN = [  # Hq, Hkv, d, query lengths, key lengths (None: the same)
+    (1, 1, 64, [1], None),
+    (4, 2, 128, [1, 2, 127, 128, 129], None),
+    (12, 12, 64, [0, 300, 0, 5, 257, 0], None),
+    (8, 1, 128, [511, 33, 1], None),
+    (6, 2, 128, [130, 260, 17], None),          # a group of 3: heads not stacked
+    (4, 4, 256, [65, 1, 200], None),
+    (32, 8, 128, [700, 64, 1300], None),
+    (2, 1, 64, [40, 1, 300, 9], [700, 129, 1, 0]),   # longer, shorter and no keys: rows that see none
+    (8, 2, 256, [3, 150], [400, 100]),
+    (4, 1, 128, [256, 512], [1024, 512]),
+    (16, 16, 128, [1] * 40, None),
+]
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("case", range(len(VARLEN)))
+def test_varlen(case, causal):
+    torch, ea, su = setup()
+    Hq, Hkv, d, lq, lk = VARLEN[case]
+    lk = lq if lk is None else lk
+    Tq, Tk = sum(lq), sum(lk)
+    q = rand(torch, Tq, Hq, d, seed=case)
+    kv = rand(torch, Tk, 2 * Hkv, d, seed=case + 100)
+    k, v = kv[:, :Hkv], kv[:, Hkv:]
+    scale = 1 / math.sqrt(d)
+    o, lse = ea.attention_varlen(q, k, v, su.starts(lq), su.starts(lk), causal=causal)
+    su.no_device_error(ea)
+    a = b = 0
+    for n, m in zip(lq, lk):
+        ref = su.attention(q[a:a + n], k[b:b + m], v[b:b + m], causal, scale)
+        if n:
+            su.check_attention(o[a:a + n], lse[:, a:a + n], ref, d)
+        a, b = a + n, b + m
+
+
+def test_varlen_matches_each_sequence_alone():
+    """A sequence's rows do not depend on its neighbours: the same bits packed and by itself."""
+    torch, ea, su = setup()
+    lens = [333, 1, 640, 128]
+    x = rand(torch, sum(lens), 12, 128, seed=4)
+    q, k, v = x[:, :8], x[:, 8:10], x[:, 10:]
+    o, lse = ea.attention_varlen(q, k, v, su.starts(lens), su.starts(lens), causal=True)
+    a = 0
+    for n in lens:
+        s = slice(a, a + n)
+        o1, l1 = ea.attention_varlen(q[s], k[s], v[s], su.i32(0, n), su.i32(0, n), causal=True)
+        assert torch.equal(o1, o[s]) and torch.equal(l1, lse[:, s])
+        a += n
+
+
+@pytest.mark.parametrize("d,Hq,Hkv", [(64, 2, 2), (128, 4, 1), (256, 2, 1)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_varlen_neighbours_hold_nan(d, Hq, Hkv, causal):
+    """NaN and infinities in other sequences, and in the rows of a padded batch, reach no other row; rows outside
+    every sequence stay as they were."""
+    torch, ea, su = setup()
+    lens = [70, 33, 140, 50]
+    front, back = 3, 21
+    T = front + sum(lens) + back
+    q, kv = rand(torch, T, Hq, d, seed=1), rand(torch, T, 2 * Hkv, d, seed=2)
+    cu = su.starts(lens) + front
+    bad = torch.zeros(T, dtype=torch.bool, device="cuda")
+    bad[:front] = bad[front + sum(lens):] = True
+    bad[front + 70:front + 103] = True  # the whole second sequence
+    q[bad], kv[bad] = math.nan, math.nan
+    kv[front + 80] = math.inf
+    k, v = kv[:, :Hkv], kv[:, Hkv:]
+    o = torch.full((T, Hq, d), 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((Hq, T), 5.0, device="cuda")
+    ea.attention_varlen(q, k, v, cu, cu, causal=causal, o=o, lse=lse)
+    su.no_device_error(ea)
+    a = front
+    for i, n in enumerate(lens):
+        s = slice(a, a + n)
+        if i == 1:
+            assert bool(torch.isnan(o[s]).all()) and bool(torch.isnan(lse[:, s]).all())
+        else:
+            su.check_attention(o[s], lse[:, s], su.attention(q[s], k[s], v[s], causal, 1 / math.sqrt(d)), d)
+        a += n
+    assert bool((o[:front] == 5).all()) and bool((o[-back:] == 5).all())
+    assert bool((lse[:, :front] == 5).all()) and bool((lse[:, -back:] == 5).all())
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.09, 0.7])
+def test_varlen_scales_without_lse(scale):
+    torch, ea, su = setup()
+    q, k, v = (rand(torch, 200, 2, 128, seed=i) for i in range(3))
+    cu = su.i32(0, 90, 200)
+    o = ea.attention_varlen(q, k, v, cu, cu, causal=True, scale=scale, return_lse=False)
+    for s in (slice(0, 90), slice(90, 200)):
+        su.check_attention(o[s], None, su.attention(q[s], k[s], v[s], True, scale), 128)
+
+
+def test_varlen_bad_boundaries_stay_inside():
+    """Boundaries outside the tensor or out of order are clamped and reported."""
+    torch, ea, su = setup()
+    q, k, v = (rand(torch, 100, 2, 64, seed=i) for i in range(3))
+    for cu in (su.i32(0, 50, 400), su.i32(-9, 50, 100), su.i32(0, 60, 40)):
+        ea.attention_varlen(q, k, v, cu, cu, causal=True)
+        assert ea.attn_get_last_device_error()[0] == 6
+    good = su.i32(0, 50, 100)
+    o, lse = ea.attention_varlen(q, k, v, good, good, causal=True)
+    su.no_device_error(ea)
+    su.check_attention(o[:50], lse[:, :50], su.attention(q[:50], k[:50], v[:50], True, 0.125), 64)
+
+
+PAGED = [  # Hq, Hkv, d, new tokens, cached tokens, page size
+    (1, 1, 64, [1], [1], 16),
+    (32, 8, 128, [1, 1, 1], [1000, 16, 17], 16),
+    (32, 8, 128, [1] * 5, [64, 63, 65, 4000, 1], 64),
+    (12, 12, 64, [1, 1], [333, 129], 32),
+    (8, 1, 256, [1, 1], [700, 50], 16),
+    (6, 2, 128, [1, 1], [257, 90], 16),            # a group of 3
+    (32, 1, 128, [1, 2], [900, 300], 128),         # 64 rows of one group
+    (4, 2, 128, [5, 1, 0, 3], [40, 1, 77, 3], 16),  # several new tokens, one sequence without
+    (8, 8, 64, [17, 40], [800, 40], 256),
+    (8, 2, 128, [300, 129, 1], [900, 129, 2000], 16),   # chunks
+    (8, 2, 128, [300, 129, 1], [900, 129, 2000], 256),
+    (16, 16, 64, [100, 260], [1500, 260], 64),
+    (4, 1, 256, [90, 33], [500, 600], 32),
+    (6, 2, 128, [200, 70], [650, 1100], 128),
+    (4, 2, 64, [60, 50], [20, 0], 16),             # rows that see no key
+    (2, 1, 128, [70], [4100], 4096),
+]
+
+
+@pytest.mark.parametrize("n_splits", [0, 1, 3])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("case", range(len(PAGED)))
+def test_paged(case, e4m3, causal, n_splits):
+    """Every unwritten slot of the cache holds NaN, and unused table entries hold no page."""
+    torch, ea, su = setup()
+    Hq, Hkv, d, new, lens, page = PAGED[case]
+    cache, table, ks, vs = su.make_cache(ea, lens, page, Hkv, d, e4m3, seed=case)
+    q = rand(torch, sum(new), Hq, d, seed=case + 50)
+    o = torch.full(q.shape, 9.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((Hq, sum(new)), 9.0, device="cuda")
+    ea.attention_paged(q, cache, table, su.i32(*lens), cu_q=su.starts(new), max_q=max(new), causal=causal,
+                       n_splits=n_splits, o=o, lse=lse)
+    su.no_device_error(ea)
+    a = 0
+    for n, k, v in zip(new, ks, vs):
+        s = slice(a, a + n)
+        if n:
+            su.check_attention(o[s], lse[:, s], su.attention(q[s], k, v, causal, 1 / math.sqrt(d)), d)
+        a += n
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n", [1, 7, 130])
+def test_paged_uniform_and_bounds(n, e4m3):
+    """Without boundaries every sequence has the same number of rows; a tighter max_kv changes the windows only."""
+    torch, ea, su = setup()
+    lens = [200, 513, 140]
+    cache, table, ks, vs = su.make_cache(ea, lens, 16, 2, 128, e4m3, seed=n, width=64)
+    q = rand(torch, 3 * n, 8, 128, seed=n)
+    for max_kv in (None, 513):
+        o, lse = ea.attention_paged(q, cache, table, su.i32(*lens), max_kv=max_kv)
+        su.no_device_error(ea)
+        for i in range(3):
+            s = slice(i * n, i * n + n)
+            su.check_attention(o[s], lse[:, s], su.attention(q[s], ks[i], vs[i], True, 1 / math.sqrt(128)), 128)
+
+
+@pytest.mark.parametrize("n", [1, 90])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_paged_bad_indices(n, e4m3):
+    """A page outside the cache reads as zeros, lengths outside their arrays are clamped; both are reported."""
+    torch, ea, su = setup()
+    cache, table, ks, vs = su.make_cache(ea, [256, 200], 16, 2, 64, e4m3, seed=3)
+    q = rand(torch, 2 * n, 4, 64, seed=8)
+    bad = table.clone()
+    bad[0, 3] = 1 << 30
+    o, lse = ea.attention_paged(q, cache, bad, su.i32(256, 200))
+    assert ea.attn_get_last_device_error()[0] == 6
+    k0, v0 = ks[0].clone(), vs[0].clone()
+    k0[48:64] = v0[48:64] = 0
+    su.check_attention(o[:n], lse[:, :n], su.attention(q[:n], k0, v0, True, 0.125), 64)
+    su.check_attention(o[n:], lse[:, n:], su.attention(q[n:], ks[1], vs[1], True, 0.125), 64)
+    o, lse = ea.attention_paged(q, cache, table, su.i32(100000, 200))  # longer than the table: its 256 keys
+    assert ea.attn_get_last_device_error()[0] == 6
+    su.check_attention(o[:n], lse[:, :n], su.attention(q[:n], ks[0], vs[0], True, 0.125), 64)
+    o, lse = ea.attention_paged(q, cache, table, su.i32(-1, 200))
+    assert ea.attn_get_last_device_error()[0] == 6
+    assert bool((o[:n] == 0).all()) and bool((lse[:, :n] == -math.inf).all())
+
+
+def test_paged_nan_row_is_nan():
+    """A cached row that was written as NaN (exponent 255) makes the rows that see it NaN and no others."""
+    torch, ea, su = setup()
+    for n in (1, 70):
+        cache, table, ks, vs = su.make_cache(ea, [100 + n, 150 + n], 16, 1, 128, True, seed=2)
+        cache.tensors[2][table[0, 2].item(), 3, 0] = 255
+        q = rand(torch, 2 * n, 2, 128, seed=1)
+        o, lse = ea.attention_paged(q, cache, table, su.i32(100 + n, 150 + n))
+        assert bool(torch.isnan(o[:n]).all()) and bool(torch.isnan(lse[:, :n]).all())
+        su.check_attention(o[n:], lse[:, n:], su.attention(q[n:], ks[1], vs[1], True, 1 / math.sqrt(128)), 128)
+
+
+def test_paged_large_scores():
+    """Scores of some hundreds: the running reference moves, one key takes each row."""
+    torch, ea, su = setup()
+    cache, table, ks, vs = su.make_cache(ea, [600], 16, 2, 128, False, seed=9)
+    for n in (1, 200):
+        q = (rand(torch, n, 8, 128, seed=n).float() * 30).to(torch.bfloat16)
+        o, lse = ea.attention_paged(q, cache, table, su.i32(600), n_splits=2)
+        su.check_attention(o, lse, su.attention(q, ks[0], vs[0], True, 1 / math.sqrt(128)), 128)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_prompt_then_steps(e4m3):
+    """As a program uses them: a prompt in two chunks, then single tokens, each written and attended, against the
+    attention of the whole sequence over the cached values."""
+    torch, ea, su = setup()
+    Hq, Hkv, d, page = 8, 2, 128, 16
+    total = [150, 61]  # tokens of the two sequences in the end
+    freqs, amp = ea.rope_freqs(d, 10000.0)
+    w = (1 + 0.1 * torch.randn(d, device="cuda")).to(torch.bfloat16)
+    rope = ea.Rope(freqs=freqs, rot_dim=d, amplitude=amp, q_weight=w, k_weight=w)
+    shape = (20, page, Hkv, d)
+    if e4m3:
+        cache = ea.KVCache(*(torch.zeros(shape, dtype=torch.uint8, device="cuda") for _ in range(2)),
+                           *(torch.zeros(shape[:3], dtype=torch.uint8, device="cuda") for _ in range(2)))
+    else:
+        cache = ea.KVCache(*(torch.full(shape, math.nan, dtype=torch.bfloat16, device="cuda") for _ in range(2)))
+    table = torch.randperm(20, device="cuda").to(torch.int32)[:20].view(2, 10)
+    x = [rand(torch, n, Hq + 2 * Hkv, d, seed=n) for n in total]
+    have, outs, qs = [0, 0], [[], []], [[], []]
+    for new in ([100, 40], [46, 17], [1, 1], [1, 1], [1, 1], [1, 1]):
+        part = torch.cat([x[i][have[i]:have[i] + n] for i, n in enumerate(new)])
+        pos = torch.cat([torch.arange(have[i], have[i] + n, device="cuda") for i, n in enumerate(new)])
+        seq = torch.repeat_interleave(torch.arange(2, device="cuda"), torch.tensor(new, device="cuda"))
+        slots = table[seq, pos // page].long() * page + pos % page
+        q = ea.kv_write(cache, part[:, Hq:Hq + Hkv], part[:, Hq + Hkv:], slots, q=part[:, :Hq], positions=pos, rope=rope)
+        have = [h + n for h, n in zip(have, new)]
+        o, _ = ea.attention_paged(q, cache, table, su.i32(*have), cu_q=su.starts(new), max_q=max(new))
+        for i, s in enumerate((slice(0, new[0]), slice(new[0], None))):
+            outs[i].append(o[s])
+            qs[i].append(q[s])
+    su.no_device_error(ea)
+    assert have == total
+    k, v = ea.kv_read(cache, table, su.starts(total), sum(total))
+    a = 0
+    for i, n in enumerate(total):
+        s = slice(a, a + n)
+        q = torch.cat(qs[i])
+        ref = su.attention(q, k[s], v[s], True, 1 / math.sqrt(d))
+        su.check_attention(torch.cat(outs[i]), None, ref, d)
+        o, _ = ea.attention_varlen(q, k[s].contiguous(), v[s].contiguous(), su.i32(0, n), su.i32(0, n), causal=True)
+        su.check_attention(o, None, ref, d)
+        a += n
+    if not e4m3:  # what went in came back: the separate pass gives the same keys
+        rk = torch.cat([ea.qk_norm_rope(x[i][:, :Hq], x[i][:, Hq:Hq + Hkv], torch.arange(n, device="cuda"), rope)[1]
+                        for i, n in enumerate(total)])
+        assert torch.equal(rk, k)
+
+
+def test_graph_replayed_with_other_lengths():
+    """Lengths, boundaries and pages are read on the device: one captured step serves later ones."""
+    torch, ea, su = setup()
+    Hq, Hkv, d = 8, 2, 128
+    cache, table, ks, vs = su.make_cache(ea, [300, 300, 300], 16, Hkv, d, True, seed=1)
+    lens, cu = su.i32(300, 300, 300), su.i32(0, 1, 2, 3)
+    q = rand(torch, 3, Hq, d, seed=1)
+    cq = su.i32(0, 100, 260)
+    x = rand(torch, 260, 4, 64, seed=2)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            ea.attention_paged(q, cache, table, lens, cu_q=cu, max_q=1, n_splits=2)
+            ea.attention_varlen(x[:, :2], x[:, 2:3], x[:, 3:], cq, cq, causal=True)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = ea.attention_paged(q, cache, table, lens, cu_q=cu, max_q=1, n_splits=2)
+        o2, l2 = ea.attention_varlen(x[:, :2], x[:, 2:3], x[:, 3:], cq, cq, causal=True)
+    for new, c in (([300, 300, 300], [0, 100, 260]), ([7, 160, 299], [0, 259, 260]), ([1, 0, 64], [0, 30, 200])):
+        lens.copy_(su.i32(*new))
+        cq.copy_(su.i32(*c))
+        graph.replay()
+        su.no_device_error(ea)
+        for i, n in enumerate(new):
+            su.check_attention(o[i:i + 1], lse[:, i:i + 1],
+                               su.attention(q[i:i + 1], ks[i][:n], vs[i][:n], True, 1 / math.sqrt(d)), d)
+        for s in (slice(c[0], c[1]), slice(c[1], c[2])):
+            su.check_attention(o2[s], l2[:, s], su.attention(x[s, :2], x[s, 2:3], x[s, 3:], True, 0.125), 64)
+
+
+def test_calls_on_two_streams():
+    """Calls with workspaces of their own may overlap."""
+    torch, ea, su = setup()
+    lens = [900, 1200, 40]
+    cache, table, ks, vs = su.make_cache(ea, lens, 16, 2, 128, False, seed=4)
+    q = rand(torch, 3, 8, 128, seed=5)
+    want = ea.attention_paged(q, cache, table, su.i32(*lens), n_splits=3)
+    x = rand(torch, 500, 6, 128, seed=6)
+    cu = su.i32(0, 130, 500)
+    want2 = ea.attention_varlen(x[:, :4], x[:, 4:5], x[:, 5:], cu, cu, causal=True)
+    kv = su.i32(*lens)
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i in range(12):
+        got.append(ea.attention_paged(q, cache, table, kv, n_splits=3, stream=s[i % 2]))
+        got.append(ea.attention_varlen(x[:, :4], x[:, 4:5], x[:, 5:], cu, cu, causal=True, stream=s[1 - i % 2]))
+    torch.cuda.synchronize()
+    su.no_device_error(ea)
+    for i in range(0, 24, 2):
+        assert all(torch.equal(a, b) for a, b in zip(got[i], want))
+        assert all(torch.equal(a, b) for a, b in zip(got[i + 1], want2))
