@@ -125,10 +125,9 @@ _lib.attn_fwd_varlen_workspace_bytes.argtypes = [_I] * 5
 _lib.attn_fwd_varlen_workspace_bytes.restype = _LL
 _lib.attn_fwd_varlen.argtypes = [_vp] * 5 + [_I] * 3 + [_vp] * 2 + [_I] * 3 + [_LL] * 3 + [_I, _F, _vp, _LL, _vp]
 _lib.attn_fwd_varlen.restype = _I
-_lib.attn_fwd_paged_workspace_bytes.argtypes = [_pc] + [_I] * 6
+_lib.attn_fwd_paged_workspace_bytes.argtypes = [_pc] + [_I] * 5
 _lib.attn_fwd_paged_workspace_bytes.restype = _LL
-_lib.attn_fwd_paged.argtypes = [_vp, _pc, _vp, _vp, _I, _I, _I, _vp, _vp, _I, _vp, _I, _I, _LL, _I, _F, _I, _vp, _LL,
-                                _vp]
+_lib.attn_fwd_paged.argtypes = [_vp, _pc, _vp, _vp, _I, _I, _I, _vp, _vp, _I, _vp, _I, _I, _LL, _I, _F, _vp, _LL, _vp]
 _lib.attn_fwd_paged.restype = _I
 
 
@@ -367,16 +366,27 @@ def attn_fwd_varlen(q, k, v, o, lse, Tq, Tk, n_seqs, cu_q, cu_k, Hq, Hkv, d, q_s
     return _check(rc, "attn_fwd_varlen", raise_on_error)
 
 
-def attn_fwd_paged_workspace_bytes(cache, Tq, n_seqs, max_q, Hq, max_kv, n_splits=0) -> int:
-    return int(_lib.attn_fwd_paged_workspace_bytes(cache, Tq, n_seqs, max_q, Hq, max_kv, n_splits))
+def attn_fwd_paged_workspace_bytes(cache, Tq, n_seqs, max_q, Hq, max_kv) -> int:
+    return int(_lib.attn_fwd_paged_workspace_bytes(cache, Tq, n_seqs, max_q, Hq, max_kv))
 
 
 def attn_fwd_paged(q, cache, o, lse, Tq, n_seqs, max_q, cu_q, table, table_width, kv_lens, max_kv, Hq, q_stride, causal,
-                   scale, n_splits, workspace, workspace_bytes, stream=None, raise_on_error=True):
+                   scale, workspace, workspace_bytes, stream=None, raise_on_error=True):
     rc = _lib.attn_fwd_paged(_ptr(q), cache, _ptr(o), _ptr(lse), Tq, n_seqs, max_q, _ptr(cu_q), _ptr(table),
-                             table_width, _ptr(kv_lens), max_kv, Hq, q_stride, int(causal), scale, n_splits,
+                             table_width, _ptr(kv_lens), max_kv, Hq, q_stride, int(causal), scale,
                              _ptr(workspace), workspace_bytes, _stream(stream))
     return _check(rc, "attn_fwd_paged", raise_on_error)
+
+
+torch = None  # the torch module, from the first use of a wrapper below
+
+
+def _load_torch():
+    global torch
+    if torch is None:
+        import torch as t
+        torch = t
+    return torch
 
 
 def _need(ok, what):
@@ -384,55 +394,63 @@ def _need(ok, what):
         raise ValueError(what)
 
 
+def _device_of(tensors):
+    """The device index that all tensors (None: skipped) are on: -1 for the host, None without a tensor."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            _need(dev is None or d == dev, "the tensors are on different devices")
+            dev = d
+    return dev
+
+
 def _on_current_device(*tensors):
-    """Every tensor is on the current CUDA device (the library launches there)."""
-    import torch
+    """Every tensor is on the current CUDA device (the library launches there); returns its index."""
     cur = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != cur):
+        if t is not None and t.get_device() != cur:
             raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
+    return cur
 
 
 def _rows(x, name):
     """Token stride of a bf16 [T, H, d] tensor whose heads are contiguous."""
-    import torch
-    if x.dim() != 3 or x.dtype != torch.bfloat16:
+    if x.dtype is not _load_torch().bfloat16 or x.dim() != 3:
         raise TypeError(f"{name} must be a bf16 tensor [T, H, d]")
     T, H, d = x.shape
-    if x.numel() == 0:
-        return H * d
     st = x.stride()
     if (st[2] != 1 and d > 1) or (st[1] != d and H > 1):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
+        if x.numel() > 0:
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
     return st[0] if T > 1 else H * d
 
 
 def _index(x, name, dtype, n=None, dim=1):
-    import torch
-    want = getattr(torch, dtype)
-    if x.dtype != want or x.dim() != dim or not x.is_contiguous():
+    if x.dtype is not getattr(_load_torch(), dtype) or x.dim() != dim or not x.is_contiguous():
         raise TypeError(f"{name} must be a contiguous {dtype} tensor of {dim} dimension(s)")
     if n is not None and x.shape[0] != n:
         raise ValueError(f"{name} has {x.shape[0]} entries, {n} are needed")
 
 
-def _on_stream(stream, *tensors):
-    """Tensors allocated here belong to the current stream: tell the allocator of another one that uses them."""
+def _use_stream(stream, dev, *new):
+    """The handle of the stream a call runs on (None: the current one).  Tensors allocated here belong to the
+    current stream: the allocator is told of another one that uses them."""
     if stream is None:
-        return
-    import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
     s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
     if s != torch.cuda.current_stream():
         s.wait_stream(torch.cuda.current_stream())  # their memory may still be in use there
-        for t in tensors:
+        for t in new:
             if t is not None:
                 t.record_stream(s)
+    return s.cuda_stream
 
 
 def rope_freqs(rot_dim, base, kind="plain", factor=1.0, trained_len=0.0, fast_turns=32.0, slow_turns=1.0,
                device="cuda"):
     """(frequencies as an fp64 tensor on `device`, amplitude) for Rope()."""
-    import torch
+    _load_torch()
     f, amp = attn_rope_freqs(rot_dim, base, ROPE_KINDS[kind], factor, trained_len, fast_turns, slow_turns)
     return torch.tensor(f, dtype=torch.float64, device=device), amp
 
@@ -442,7 +460,7 @@ class Rope:
 
     def __init__(self, freqs=None, rot_dim=0, interleaved=False, amplitude=1.0, q_weight=None, k_weight=None,
                  eps=1e-6):
-        import torch
+        _load_torch()
         _need(rot_dim == 0 or freqs is not None, "freqs are needed where rot_dim > 0")
         if freqs is not None and rot_dim > 0:
             _index(freqs, "freqs", "float64", rot_dim // 2)
@@ -455,6 +473,7 @@ class Rope:
                 d = w.shape[0]
         self.d = d  # the head size the weights are for, None without weights
         self.tensors = (freqs, q_weight, k_weight)
+        self.device = _device_of(self.tensors)
         self.rot_dim = rot_dim
         self.struct = _RopeStruct(_ptr(q_weight), _ptr(k_weight), _ptr(freqs) if rot_dim > 0 else None, eps, amplitude,
                                   rot_dim, int(interleaved))
@@ -466,7 +485,7 @@ class KVCache:
     bytes k_exp and v_exp [n_pages, page_size, Hkv] in uint8."""
 
     def __init__(self, k_pages, v_pages, k_exp=None, v_exp=None):
-        import torch
+        _load_torch()
         if k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8) or v_pages.dtype != k_pages.dtype:
             raise TypeError("k_pages and v_pages must both be bf16, float8_e4m3fn or uint8")
         _need(k_pages.dim() == 4 and k_pages.shape == v_pages.shape, "k_pages and v_pages must be [n_pages, page_size, Hkv, d]")
@@ -478,6 +497,7 @@ class KVCache:
         for t in (k_pages, v_pages, k_exp, v_exp):
             _need(t is None or t.is_contiguous(), "the cache's tensors must be contiguous")
         self.tensors = (k_pages, v_pages, k_exp, v_exp)
+        self.device = _device_of(self.tensors)
         self.n_pages, self.page_size, self.Hkv, self.d = k_pages.shape
         self.struct = _CacheStruct(_ptr(k_pages), _ptr(v_pages), _ptr(k_exp), _ptr(v_exp), self.n_pages,
                                    self.page_size, self.Hkv, self.d, ATTN_FP8_E4M3 if e4m3 else ATTN_BF16)
@@ -490,91 +510,120 @@ def _check_rope_use(rope, d, positions, T):
         _index(positions, "positions", "int64", T)
 
 
+def _handle_device(handle, dev):
+    if handle.device != dev and handle.device is not None:
+        raise ValueError(f"the tensors of the {type(handle).__name__} are not on the current device cuda:{dev}")
+
+
+def _like(x):
+    """A new contiguous tensor like x."""
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+
+
 def qk_norm_rope(q, k, positions, rope, q_out=None, k_out=None, stream=None):
     """q [T, Hq, d] and k [T, Hkv, d] (bf16, slices of a fused projection allowed) normed and rotated;
     returns (q_out, k_out), new contiguous tensors unless given (q_out=q and k_out=k work in place)."""
-    import torch
+    qs, ks = _rows(q, "q"), _rows(k, "k")
     T, Hq, d = q.shape
-    Hkv = k.shape[1]
-    _need(k.shape[0] == T and k.shape[2] == d, "q and k must have the same tokens and head size")
+    Tk, Hkv, dk = k.shape
+    _need(Tk == T and dk == d, "q and k must have the same tokens and head size")
     _check_rope_use(rope, d, positions, T)
-    _on_current_device(q, k, positions, q_out, k_out, *rope.tensors)
-    new = []
+    dev = _on_current_device(q, k, positions, q_out, k_out)
+    _handle_device(rope, dev)
+    new_q = new_k = None
+    qos, kos = Hq * d, Hkv * d
     if q_out is None:
-        q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
-        new.append(q_out)
+        q_out = new_q = _like(q)
+    else:
+        _need(q_out.shape == q.shape, "q_out must have q's shape")
+        qos = _rows(q_out, "q_out")
     if k_out is None:
-        k_out = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=q.device)
-        new.append(k_out)
-    _need(q_out.shape == q.shape and k_out.shape == k.shape, "the outputs must have the inputs' shapes")
-    _on_stream(stream, *new)
-    attn_qk_norm_rope(q, k, q_out, k_out, T, Hq, Hkv, d, _rows(q, "q"), _rows(k, "k"), _rows(q_out, "q_out"),
-                      _rows(k_out, "k_out"), positions, rope.struct, stream)
+        k_out = new_k = _like(k)
+    else:
+        _need(k_out.shape == k.shape, "k_out must have k's shape")
+        kos = _rows(k_out, "k_out")
+    rc = _lib.attn_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), T, Hq, Hkv, d, qs, ks,
+                                qos, kos, _ptr(positions), rope.struct, _use_stream(stream, dev, new_q, new_k))
+    if rc:
+        raise AttnError(rc, "attn_qk_norm_rope")
     return q_out, k_out
 
 
 def kv_write(cache, k, v, slots, q=None, positions=None, rope=None, q_out=None, stream=None):
     """Keys and values [T, Hkv, d] (bf16) into the cache's slots (int64 [T], negative: skipped).  With rope the
     keys are normed and rotated on the way, and so are the queries q [T, Hq, d], which are returned."""
-    import torch
+    ks, vs = _rows(k, "k"), _rows(v, "v")
     T = k.shape[0]
     _need(k.shape == v.shape == (T, cache.Hkv, cache.d), "k and v must be [T, Hkv, d] of the cache")
     _index(slots, "slots", "int64", T)
     _need(rope is not None or q is None, "queries only take part where rope is given")
-    _on_current_device(k, v, slots, q, positions, q_out, *cache.tensors, *(rope.tensors if rope is not None else ()))
+    dev = _on_current_device(k, v, slots, q, positions, q_out)
+    _handle_device(cache, dev)
+    rs = None
     if rope is not None:
         _check_rope_use(rope, cache.d, positions, T)
+        _handle_device(rope, dev)
+        rs = rope.struct
     Hq = qs = qos = 0
+    new = None
     if q is not None:
+        qs = _rows(q, "q")
         Hq = q.shape[1]
         _need(q.shape[0] == T and q.shape[2] == cache.d, "q must have k's tokens and head size")
         if q_out is None:
-            q_out = torch.empty((T, Hq, cache.d), dtype=torch.bfloat16, device=q.device)
-            _on_stream(stream, q_out)
-        _need(q_out.shape == q.shape, "q_out must have q's shape")
-        qs, qos = _rows(q, "q"), _rows(q_out, "q_out")
-    attn_kv_write(cache.struct, k, v, T, _rows(k, "k"), _rows(v, "v"), slots, rope.struct if rope is not None else None,
-                  positions, q, q_out, Hq, qs, qos, stream)
+            q_out = new = _like(q)
+            qos = Hq * cache.d
+        else:
+            _need(q_out.shape == q.shape, "q_out must have q's shape")
+            qos = _rows(q_out, "q_out")
+    rc = _lib.attn_kv_write(cache.struct, k.data_ptr(), v.data_ptr(), T, ks, vs, slots.data_ptr(), rs, _ptr(positions),
+                            _ptr(q), _ptr(q_out), Hq, qs, qos, _use_stream(stream, dev, new))
+    if rc:
+        raise AttnError(rc, "attn_kv_write")
     return q_out
 
 
 def kv_read(cache, table, cu, T, k_out=None, v_out=None, stream=None):
     """The cached tokens of each sequence (pages table[s], int32; boundaries cu of the T output rows, int32
     [n_seqs + 1]) as packed bf16 keys and values [T, Hkv, d]."""
-    import torch
-    n = table.shape[0]
     _index(table, "table", "int32", dim=2)
+    n, width = table.shape
     _index(cu, "cu", "int32", n + 1)
-    _on_current_device(table, cu, k_out, v_out, *cache.tensors)
-    shape, new = (T, cache.Hkv, cache.d), []
+    dev = _on_current_device(table, cu, k_out, v_out)
+    _handle_device(cache, dev)
+    shape = (T, cache.Hkv, cache.d)
+    new = []
+    for t in (k_out, v_out):
+        _need(t is None or (t.shape == shape and t.dtype is torch.bfloat16 and t.is_contiguous()),
+              "k_out and v_out must be contiguous bf16 [T, Hkv, d]")
     if k_out is None:
         k_out = torch.empty(shape, dtype=torch.bfloat16, device=table.device)
         new.append(k_out)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=table.device)
+        v_out = torch.empty_like(k_out)
         new.append(v_out)
-    for t in (k_out, v_out):
-        _need(tuple(t.shape) == shape and t.dtype == torch.bfloat16 and t.is_contiguous(),
-              "k_out and v_out must be contiguous bf16 [T, Hkv, d]")
-    _on_stream(stream, *new)
-    attn_kv_read(cache.struct, table, table.shape[1], cu, n, k_out, v_out, T, stream)
+    rc = _lib.attn_kv_read(cache.struct, table.data_ptr(), width, cu.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(), T,
+                           _use_stream(stream, dev, *new))
+    if rc:
+        raise AttnError(rc, "attn_kv_read")
     return k_out, v_out
 
 
 def _outputs(q, o, lse, return_lse):
     """(o, lse, tensors made here)"""
-    import torch
-    T, H, d = q.shape
+    T, H, _ = q.shape
     new = []
     if o is None:
-        o = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
+        o = _like(q)
         new.append(o)
-    if lse is None and return_lse:
+    else:
+        _need(o.shape == q.shape and o.dtype is torch.bfloat16 and o.is_contiguous(), "o must be contiguous bf16 like q")
+    if lse is not None:
+        _need(lse.shape == (H, T) and lse.dtype is torch.float32 and lse.is_contiguous(),
+              "lse must be contiguous fp32 [Hq, T]")
+    elif return_lse:
         lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
         new.append(lse)
-    _need(o.shape == q.shape and o.dtype == torch.bfloat16 and o.is_contiguous(), "o must be contiguous bf16 like q")
-    _need(lse is None or (tuple(lse.shape) == (H, T) and lse.dtype == torch.float32 and lse.is_contiguous()),
-          "lse must be contiguous fp32 [Hq, T]")
     return o, lse, new
 
 
@@ -583,34 +632,39 @@ def attention_varlen(q, k, v, cu_q, cu_k, causal: bool = False, scale: float | N
     """O [Tq, Hq, d] (and LSE [Hq, Tq]) of packed sequences: q [Tq, Hq, d], k/v [Tk, Hkv, d] (bf16, slices of a
     fused projection allowed), boundaries cu_q, cu_k int32 [n_seqs + 1].  Rows outside every sequence are
     not written."""
-    import torch
+    qs, ks, vs = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
     Tq, Hq, d = q.shape
-    Tk, Hkv, _ = k.shape
-    _need(k.shape == v.shape and k.shape[2] == d, "k and v must have the same shape, and q's head size")
-    n = cu_q.shape[0] - 1
+    Tk, Hkv, dk = k.shape
+    _need(k.shape == v.shape and dk == d, "k and v must have the same shape, and q's head size")
     _index(cu_q, "cu_q", "int32")
+    n = cu_q.shape[0] - 1
     _index(cu_k, "cu_k", "int32", n + 1)
-    _on_current_device(q, k, v, cu_q, cu_k, o, lse)
+    dev = _on_current_device(q, k, v, cu_q, cu_k, o, lse)
     o, lse, new = _outputs(q, o, lse, return_lse)
-    nbytes = attn_fwd_varlen_workspace_bytes(Tq, n, Hq, Hkv, d)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes > 0 else None
-    _on_stream(stream, ws, *new)
-    attn_fwd_varlen(q, k, v, o, lse, Tq, Tk, n, cu_q, cu_k, Hq, Hkv, d, _rows(q, "q"), _rows(k, "k"), _rows(v, "v"),
-                    causal, 1.0 / math.sqrt(d) if scale is None else scale, ws, max(nbytes, 0), stream)
+    nbytes = _lib.attn_fwd_varlen_workspace_bytes(Tq, n, Hq, Hkv, d)
+    ws = None
+    if nbytes > 0:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        new.append(ws)
+    rc = _lib.attn_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(lse), Tq, Tk, n,
+                              cu_q.data_ptr(), cu_k.data_ptr(), Hq, Hkv, d, qs, ks, vs, int(causal),
+                              1.0 / math.sqrt(d) if scale is None else scale, _ptr(ws), max(nbytes, 0),
+                              _use_stream(stream, dev, *new))
+    if rc:
+        raise AttnError(rc, "attn_fwd_varlen")
     return (o, lse) if return_lse else o
 
 
 def attention_paged(q, cache, table, kv_lens, cu_q=None, max_q=None, max_kv=None, causal: bool = True,
-                    scale: float | None = None, n_splits: int = 0, return_lse: bool = True, o=None, lse=None,
-                    stream=None):
+                    scale: float | None = None, return_lse: bool = True, o=None, lse=None, stream=None):
     """O [Tq, Hq, d] (and LSE [Hq, Tq]) of new tokens q over the cache, which holds them already: table int32
     [n_seqs, width], kv_lens int32 [n_seqs] with the new tokens counted.  cu_q int32 [n_seqs + 1] gives the
     sequences' rows of q and max_q bounds their number; without cu_q every sequence has Tq / n_seqs rows."""
-    import torch
+    qs = _rows(q, "q")
     Tq, Hq, d = q.shape
-    n = table.shape[0]
     _need(d == cache.d, "q and the cache differ in head size")
     _index(table, "table", "int32", dim=2)
+    n, width = table.shape
     _index(kv_lens, "kv_lens", "int32", n)
     if cu_q is not None:
         _index(cu_q, "cu_q", "int32", n + 1)
@@ -618,13 +672,20 @@ def attention_paged(q, cache, table, kv_lens, cu_q=None, max_q=None, max_kv=None
     else:
         _need(n > 0 and Tq % n == 0 and max_q in (None, Tq // n), "without cu_q every sequence has Tq / n_seqs rows")
         max_q = Tq // n
-    width = table.shape[1]
-    max_kv = width * cache.page_size if max_kv is None else max_kv
-    _on_current_device(q, table, kv_lens, cu_q, o, lse, *cache.tensors)
+    if max_kv is None:
+        max_kv = width * cache.page_size
+    dev = _on_current_device(q, table, kv_lens, cu_q, o, lse)
+    _handle_device(cache, dev)
     o, lse, new = _outputs(q, o, lse, return_lse)
-    nbytes = attn_fwd_paged_workspace_bytes(cache.struct, Tq, n, max_q, Hq, max_kv, n_splits)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes > 0 else None
-    _on_stream(stream, ws, *new)
-    attn_fwd_paged(q, cache.struct, o, lse, Tq, n, max_q, cu_q, table, width, kv_lens, max_kv, Hq, _rows(q, "q"), causal,
-                   1.0 / math.sqrt(d) if scale is None else scale, n_splits, ws, max(nbytes, 0), stream)
+    nbytes = _lib.attn_fwd_paged_workspace_bytes(cache.struct, Tq, n, max_q, Hq, max_kv)
+    ws = None
+    if nbytes > 0:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        new.append(ws)
+    rc = _lib.attn_fwd_paged(q.data_ptr(), cache.struct, o.data_ptr(), _ptr(lse), Tq, n, max_q, _ptr(cu_q),
+                             table.data_ptr(), width, kv_lens.data_ptr(), max_kv, Hq, qs, int(causal),
+                             1.0 / math.sqrt(d) if scale is None else scale, _ptr(ws), max(nbytes, 0),
+                             _use_stream(stream, dev, *new))
+    if rc:
+        raise AttnError(rc, "attn_fwd_paged")
     return (o, lse) if return_lse else o

@@ -169,7 +169,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // mutex.
 struct MapKey {
   uint64_t ptr;
-  uint32_t dtype, rank;
+  uint32_t dtype, rank, swizzle, promotion;
   cuuint64_t dims[5], strides[4];
   cuuint32_t box[5];
 };
@@ -188,12 +188,16 @@ std::mutex g_maps_mu;
 std::atomic<unsigned long long> g_map_hits{0}, g_map_encodes{0};
 
 int encode_cached(CUtensorMap* m, CUtensorMapDataType dt, uint32_t rank, const void* ptr, const cuuint64_t* dims,
-                  const cuuint64_t* strides, const cuuint32_t* box) {
+                  const cuuint64_t* strides, const cuuint32_t* box,
+                  CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B,
+                  CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
   MapKey key;
   std::memset(&key, 0, sizeof(key));  // padding bytes take part in the comparison
   key.ptr = reinterpret_cast<uint64_t>(ptr);
   key.dtype = (uint32_t)dt;
   key.rank = rank;
+  key.swizzle = (uint32_t)swizzle;
+  key.promotion = (uint32_t)promotion;
   for (uint32_t i = 0; i < rank; ++i) {
     key.dims[i] = dims[i];
     key.box[i] = box[i];
@@ -214,8 +218,8 @@ int encode_cached(CUtensorMap* m, CUtensorMapDataType dt, uint32_t rank, const v
   }
   const cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
   const CUresult r = g_encode(m, dt, rank, const_cast<void*>(ptr), dims, strides, box, estr,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return ATTN_ERR_CUDA;
   g_map_encodes.fetch_add(1, std::memory_order_relaxed);
   std::lock_guard<std::mutex> lk(g_maps_mu);
@@ -267,13 +271,28 @@ int encode_packed_groups(CUtensorMap* m, const void* ptr, int T, int H, int g, i
   const cuuint32_t box[5] = {64u, (cuuint32_t)g, 1u, (cuuint32_t)(rows / g), 1u};
   return encode_cached(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, ptr, dims, strides, box);
 }
-// Pages [n_pages, page_size, Hkv, d] of a bf16 cache: a box is one head x
-// `rows` tokens of one page.
+// Pages [n_pages, page_size, Hkv, d] of a cache: a box is one head x
+// `rows` tokens of one page.  A fetch is widened to no more than a head's row: the
+// next head's bytes are another block's, read at another time (with 256 bytes a
+// 128-byte row cost 1.5 times its traffic).  The e4m3 form has boxes of up to 128
+// codes a row (64 with the 64-byte swizzle at d = 64).
+CUtensorMapL2promotion row_promotion(int bytes) {
+  return bytes >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                      : (bytes >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B);
+}
+int encode_pages_e4m3(CUtensorMap* m, const void* ptr, int n_pages, int page_size, int Hkv, int d, int rows) {
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)Hkv, (cuuint64_t)page_size, (cuuint64_t)n_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)d, (cuuint64_t)Hkv * d, (cuuint64_t)page_size * Hkv * d};
+  const cuuint32_t box[4] = {(cuuint32_t)(d < 128 ? d : 128), 1u, (cuuint32_t)rows, 1u};
+  return encode_cached(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, ptr, dims, strides, box,
+                       d < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, row_promotion(d));
+}
 int encode_pages(CUtensorMap* m, const void* ptr, int n_pages, int page_size, int Hkv, int d, int rows) {
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)Hkv, (cuuint64_t)page_size, (cuuint64_t)n_pages};
   const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)Hkv * d * 2, (cuuint64_t)page_size * Hkv * d * 2};
   const cuuint32_t box[4] = {64u, 1u, (cuuint32_t)rows, 1u};
-  return encode_cached(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, ptr, dims, strides, box);
+  return encode_cached(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, ptr, dims, strides, box,
+                       CU_TENSOR_MAP_SWIZZLE_128B, row_promotion(2 * d));
 }
 
 // 2-D row-major bf16 matrix [rows, cols] as a 4-D map (cols, rows, 1, 1), box

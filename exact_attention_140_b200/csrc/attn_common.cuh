@@ -17,6 +17,7 @@ struct RaggedParams {
   int Tq;            // query tokens in all (lse rows)
   const int* table;  // paged: page table [n_seqs, table_width]
   int table_width, page_shift, n_pages;
+  const unsigned char *k_exp, *v_exp;  // e4m3 cache: exponent bytes [n_pages, page_size, Hkv]
 };
 
 struct FwdParams {
@@ -96,8 +97,14 @@ template <int D_, int BN_, int NQT_, int KST_, int VST_, bool CAUSAL_, bool FP8_
           int RAGGED_ = 0>
 struct FwdCfg {
   // RAGGED (one-block-per-item kernel): 1 packed sequences, 2 packed queries
-  // over a paged cache; 0 the dense [B, N, H, d] tensors
+  // over a paged bf16 cache, 3 over a paged e4m3 cache (KV8: the codes arrive in
+  // a ring of their own and a warpgroup expands them into the bf16 key and value
+  // tiles); 0 the dense [B, N, H, d] tensors
   static constexpr int RAGGED = RAGGED_;
+  static constexpr bool KV8 = RAGGED == 3;
+  static constexpr int RST = D_ == 64 ? 4 : 2;                     // stages of the code ring
+  static constexpr uint32_t RAW_BYTES = (uint32_t)BN_ * D_;        // codes of a key or value tile
+  static constexpr int BOX8 = D_ < 128 ? D_ : 128, NCH8 = D_ / BOX8;  // codes of a box row, boxes across a row
   // PACK: the one-block-per-item kernel reads the head-packing factor from the
   // launch parameters (split-KV); otherwise it is compiled out
   static constexpr bool PACK = PACK_;
@@ -157,14 +164,19 @@ struct FwdCfg {
   static constexpr int B_QEMPTY = B_OFREE + NQT;
   static constexpr int B_SFREE = B_QEMPTY + 1;  // S read out of tensor memory (PSEP)
   static constexpr int B_DRAIN = B_SFREE + NQT * SB;
-  static constexpr int NBAR = B_DRAIN + 1;
+  static constexpr int B_RFULL = B_DRAIN + 1;  // KV8: code ring
+  static constexpr int B_REMPTY = B_RFULL + (KV8 ? RST : 0);
+  static constexpr int NBAR = B_REMPTY + (KV8 ? RST : 0);
   // shared memory (offsets from a 1024-byte aligned base; stream s adds
   // s * STREAM_BYTES to the tile offsets and s * NBAR to barrier indices)
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_K = OFF_Q + NQT * QT_BYTES;
   static constexpr uint32_t OFF_V = OFF_K + KST * KV_BYTES;
   static constexpr uint32_t OFF_OST = OFF_V + VST * KV_BYTES;  // output staging tile (OST)
-  static constexpr uint32_t STREAM_BYTES = OFF_OST + (OST ? (uint32_t)BM * D * 2 : 0u);
+  static constexpr uint32_t OFF_RAW = OFF_OST;                 // code ring (KV8)
+  static_assert(!KV8 || !OST, "one of the two follows the V ring");
+  static constexpr uint32_t STREAM_BYTES =
+      OFF_OST + (OST ? (uint32_t)BM * D * 2 : 0u) + (KV8 ? RST * RAW_BYTES : 0u);
   static constexpr uint32_t OFF_BAR = NS * STREAM_BYTES;
   static constexpr uint32_t OFF_SLOT = OFF_BAR + NS * NBAR * 8;
   static constexpr uint32_t OFF_ABORT = OFF_SLOT + 4;
@@ -178,14 +190,17 @@ struct FwdCfg {
   static constexpr int SM_WARPS = 4 * NQT * NS;
   static constexpr int TMA_WARP = SM_WARPS;
   static constexpr int MMA_WARP = SM_WARPS + 1;
-  static constexpr int NTHREADS = 32 * (SM_WARPS + 4);
+  static constexpr int XP_WARP = SM_WARPS + 4;  // KV8: four more warps that expand the codes
+  static constexpr int XP_WARPS = KV8 ? 4 : 0;
+  static constexpr int NTHREADS = 32 * (SM_WARPS + 4 + XP_WARPS);
   // register split (two softmax warpgroups: 384 threads launch with 168
   // registers each = 64512; the softmax warpgroups get 200, the control
   // warpgroup 104: 2*128*200 + 128*104 = 64512)
   static constexpr int REG_LAUNCH = 65536 / NTHREADS >= 255 ? 255 : (65536 / NTHREADS) / 8 * 8;
   static constexpr bool SPLIT_REGS = NQT * NS == 2;
-  static constexpr int REG_SOFTMAX = 200, REG_CONTROL = 104;
-  static_assert(!SPLIT_REGS || 2 * 128 * REG_SOFTMAX + 128 * REG_CONTROL <= NTHREADS * REG_LAUNCH,
+  // (KV8: 512 threads launch with 128; 2*128*200 + 2*128*56 = 65536)
+  static constexpr int REG_SOFTMAX = 200, REG_CONTROL = KV8 ? 56 : 104;
+  static_assert(!SPLIT_REGS || 2 * 128 * REG_SOFTMAX + (NTHREADS - 256) * REG_CONTROL <= NTHREADS * REG_LAUNCH,
                 "register split exceeds the launch allocation");
   static constexpr uint32_t IDESC_QK = ptx::idesc<FP8>(128, BN, false);
   static constexpr uint32_t IDESC_PV = ptx::idesc<FP8>(128, D, true);

@@ -54,6 +54,7 @@
 #include <type_traits>
 
 #include "attn_common.cuh"
+#include "e4m3.cuh"
 #include "exp2_soft.cuh"
 #include "ptx.cuh"
 #include "tiles.h"
@@ -147,11 +148,11 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
   if (threadIdx.x == 0) {
     for (int t = 0; t < NQT; ++t) ptx::mbar_init(bar(Cfg::B_QFULL + t), 1);
     for (int s = 0; s < KST; ++s) {
-      ptx::mbar_init(bar(Cfg::B_KFULL + s), 1);
+      ptx::mbar_init(bar(Cfg::B_KFULL + s), Cfg::KV8 ? 32 * Cfg::XP_WARPS : 1);
       ptx::mbar_init(bar(Cfg::B_KEMPTY + s), 1);
     }
     for (int s = 0; s < VST; ++s) {
-      ptx::mbar_init(bar(Cfg::B_VFULL + s), 1);
+      ptx::mbar_init(bar(Cfg::B_VFULL + s), Cfg::KV8 ? 32 * Cfg::XP_WARPS : 1);
       ptx::mbar_init(bar(Cfg::B_VEMPTY + s), 1);
     }
     for (int i = 0; i < NQT * SB; ++i) {
@@ -162,6 +163,12 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
     for (int t = 0; t < NQT; ++t) {
       ptx::mbar_init(bar(Cfg::B_ODONE + t), 1);
       ptx::mbar_init(bar(Cfg::B_OFINAL + t), 1);
+    }
+    if constexpr (Cfg::KV8) {
+      for (int i = 0; i < Cfg::RST; ++i) {
+        ptx::mbar_init(bar(Cfg::B_RFULL + i), 1);
+        ptx::mbar_init(bar(Cfg::B_REMPTY + i), 32 * Cfg::XP_WARPS);
+      }
     }
     ptx::mbar_init(bar(Cfg::B_DRAIN), 1);
     *abort_flag = 0u;
@@ -436,13 +443,14 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
     if constexpr (Cfg::SPLIT_REGS) ptx::setmaxnreg_dec<Cfg::REG_CONTROL>();
     // (over a paged cache the whole warp runs the loop: lane i fetches the
     // tile's page i and issues its boxes)
-    constexpr bool PAGED = Cfg::RAGGED == 2;
+    constexpr bool PAGED = Cfg::RAGGED >= 2;
     if (PAGED || lane == 0) {
       int k_issued[KST], v_issued[VST];
 #pragma unroll
       for (int s = 0; s < KST; ++s) k_issued[s] = 0;
 #pragma unroll
       for (int s = 0; s < VST; ++s) v_issued[s] = 0;
+      [[maybe_unused]] int r_issued = 0;  // code tiles
       bool q_issued[NQT];
 #pragma unroll
       for (int t = 0; t < NQT; ++t) {
@@ -467,14 +475,17 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
       // one operand's key tile: the boxes that make up its BN rows
       auto load_kv = [&](const CUtensorMap* tm, uint32_t dst, uint32_t fb, int j, int page) {
         if constexpr (PAGED) {
-          if (lane == 0) ptx::mbar_arrive_expect_tx(fb, Cfg::KV_BYTES);
+          // a row of a box is 128 bytes of bf16, or BOX8 codes
+          constexpr int NBOX = Cfg::KV8 ? Cfg::NCH8 : Cfg::NCH, BOXW = Cfg::KV8 ? Cfg::BOX8 : Cfg::BOXE;
+          constexpr uint32_t RP = Cfg::KV8 ? Cfg::BOX8 : 128u;
+          if (lane == 0) ptx::mbar_arrive_expect_tx(fb, Cfg::KV8 ? Cfg::RAW_BYTES : Cfg::KV_BYTES);
           __syncwarp();
           const int ps = 1 << p.rg.page_shift, rows = ps < BN ? ps : BN;  // rows of a box
           if (lane < BN / rows) {
             const int r0 = ps < BN ? 0 : (kv0 + j * BN) & (ps - 1);
 #pragma unroll
-            for (int c = 0; c < Cfg::NCH; ++c)
-              ptx::tma_load_4d(dst + c * Cfg::CH_KV + lane * rows * 128, tm, fb, c * Cfg::BOXE, kh, r0, page);
+            for (int c = 0; c < NBOX; ++c)
+              ptx::tma_load_4d(dst + c * (BN * RP) + lane * rows * RP, tm, fb, c * BOXW, kh, r0, page);
           }
         } else {
           ptx::mbar_arrive_expect_tx(fb, Cfg::KV_BYTES);
@@ -499,6 +510,20 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
       [[maybe_unused]] int page = page_of(0);
       for (int j = 0; j < nmax; ++j) {
         [[maybe_unused]] const int page_next = PAGED && j + 1 < nmax ? page_of(j + 1) : 0;
+        if constexpr (Cfg::KV8) {  // codes of K_j, then of V_j, through one ring
+          bool go = true;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int i = 2 * j + x, rs = i % Cfg::RST;
+            go = go && (i < Cfg::RST || wait_empty(bar(Cfg::B_REMPTY + rs), (uint32_t)((i / Cfg::RST - 1) & 1), kSiteKEmpty));
+            if (!go) continue;
+            load_kv(x == 0 ? &tmK : &tmV, sbase + Cfg::OFF_RAW + rs * Cfg::RAW_BYTES, bar(Cfg::B_RFULL + rs), j, page);
+            ++r_issued;
+          }
+          if (!go) break;
+          page = page_next;
+          continue;
+        }
         const int ks = j % KST;
         if (j >= KST && !wait_empty(bar(Cfg::B_KEMPTY + ks), (uint32_t)(((j / KST) - 1) & 1), kSiteKEmpty)) break;
         {
@@ -518,12 +543,92 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
 #pragma unroll
       for (int t = 0; t < NQT; ++t)
         if (q_issued[t]) wait_bar_drain<kRoleProducer>(bar(Cfg::B_QFULL + t), 0u, wc, kSiteQ);
+      if constexpr (Cfg::KV8) {
+#pragma unroll
+        for (int i = 0; i < Cfg::RST; ++i) {
+          const int n = (r_issued - i + Cfg::RST - 1) / Cfg::RST;  // fills of stage i
+          if (n > 0) wait_bar_drain<kRoleProducer>(bar(Cfg::B_RFULL + i), (uint32_t)((n - 1) & 1), wc, kSiteKFull);
+        }
+      }
 #pragma unroll
       for (int s = 0; s < KST; ++s)
         if (k_issued[s] > 0) wait_bar_drain<kRoleProducer>(bar(Cfg::B_KFULL + s), (uint32_t)((k_issued[s] - 1) & 1), wc, kSiteKFull);
 #pragma unroll
       for (int s = 0; s < VST; ++s)
         if (v_issued[s] > 0) wait_bar_drain<kRoleProducer>(bar(Cfg::B_VFULL + s), (uint32_t)((v_issued[s] - 1) & 1), wc, kSiteVFull);
+    }
+  } else if (Cfg::KV8 && warp >= Cfg::XP_WARP) {
+    if constexpr (Cfg::SPLIT_REGS) ptx::setmaxnreg_dec<Cfg::REG_CONTROL>();
+    if constexpr (Cfg::KV8) {
+      // ---------------------------------------------------------- expanding
+      constexpr int RPW = BN / (Cfg::KV8 ? Cfg::XP_WARPS : 1);  // rows of this warp (at most one per lane)
+      const int row0 = (warp - Cfg::XP_WARP) * RPW;
+      const uint32_t raw0 = sbase + Cfg::OFF_RAW;
+      // the page and the exponents of row row0 + lane, fetched two and one
+      // tiles ahead (the table, then the bytes behind it)
+      struct Facs { uint32_t k, v; };
+      auto fetch_id = [&](int j) -> int {
+        const int i = j * BN + row0 + lane, pi = (kv0 + i) >> p.rg.page_shift;
+        return lane < RPW && j < nmax && i < nk && pi < p.rg.table_width
+                   ? __ldg(p.rg.table + (long long)seq * p.rg.table_width + pi) : -1;
+      };
+      auto fetch_facs = [&](int j, int id) -> Facs {
+        const int key = kv0 + j * BN + row0 + lane;
+        if (id < 0 || id >= p.rg.n_pages) return Facs{0u, 0u};  // (zeros)
+        const long long at = (((long long)id << p.rg.page_shift) + (key & ((1 << p.rg.page_shift) - 1))) * p.Hkv + kh;
+        return Facs{__ldg(p.rg.k_exp + at), __ldg(p.rg.v_exp + at)};
+      };
+      auto expand = [&](uint32_t src, uint32_t dst, uint32_t ex) {
+        const bool big = __any_sync(0xffffffffu, ex > 134u);
+#pragma unroll 2
+        for (int grp = 0; grp < RPW / 8; ++grp) {
+          const int r = row0 + grp * 8 + (lane & 7);
+          const E4m3Factor f = e4m3_factor(__shfl_sync(0xffffffffu, ex, grp * 8 + (lane & 7)));
+#pragma unroll
+          for (int it = 0; it < D / 64; ++it) {
+            const int pc = (lane >> 3) + 4 * it;  // piece of 16 codes of the row
+            // (TMA permutes a row's 16-byte pieces within 128 bytes, or 64 for 64-byte rows)
+            const uint32_t pin = D == 64 ? (uint32_t)(pc ^ ((r >> 1) & 3)) : (uint32_t)((pc & 7) ^ (r & 7));
+            uint32_t w[4], o[8];
+            ptx::ld_shared_v4(src + (uint32_t)(pc * 16 / Cfg::BOX8) * (BN * Cfg::BOX8) + (uint32_t)r * Cfg::BOX8 + pin * 16u, w);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              o[2 * u] = bf16x2_mul(e4m3_hi_bits(__byte_perm(w[u], 0u, 0x1404)), f.m);
+              o[2 * u + 1] = bf16x2_mul(e4m3_hi_bits(__byte_perm(w[u], 0u, 0x3424)), f.m);
+            }
+            if (big) {
+#pragma unroll
+              for (int u = 0; u < 8; ++u) o[u] = bf16x2_mul(o[u], f.more);
+            }
+            const uint32_t drow = dst + (uint32_t)(pc / 4) * Cfg::CH_KV + (uint32_t)r * 128u;
+            const uint32_t p0 = (uint32_t)(2 * (pc & 3));
+            ptx::st_shared_v4(drow + ((p0 ^ (uint32_t)(r & 7)) << 4), o[0], o[1], o[2], o[3]);
+            ptx::st_shared_v4(drow + (((p0 + 1) ^ (uint32_t)(r & 7)) << 4), o[4], o[5], o[6], o[7]);
+          }
+        }
+        ptx::fence_proxy_async_smem();
+      };
+      Facs fac = fetch_facs(0, fetch_id(0));
+      int id = fetch_id(1);
+      for (int j = 0; j < nmax; ++j) {
+        const Facs fac_next = fetch_facs(j + 1, id);
+        id = fetch_id(j + 2);
+        bool go = true;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int i = 2 * j + x, rs = i % Cfg::RST, st = x == 0 ? j % KST : j % VST, n_st = x == 0 ? KST : VST;
+          go = go && wait_bar_warp<kRoleProducer>(bar(Cfg::B_RFULL + rs), (uint32_t)((i / Cfg::RST) & 1), wc, kSiteKFull);
+          go = go && (j < n_st || wait_bar_warp<kRoleProducer>(bar((x == 0 ? Cfg::B_KEMPTY : Cfg::B_VEMPTY) + st),
+                                                               (uint32_t)((j / n_st - 1) & 1), wc, kSiteVEmpty));
+          if (!go) continue;
+          expand(raw0 + rs * Cfg::RAW_BYTES, sbase + (x == 0 ? Cfg::OFF_K : Cfg::OFF_V) + st * Cfg::KV_BYTES,
+                 x == 0 ? fac.k : fac.v);
+          ptx::mbar_arrive(bar((x == 0 ? Cfg::B_KFULL : Cfg::B_VFULL) + st));
+          ptx::mbar_arrive(bar(Cfg::B_REMPTY + rs));
+        }
+        if (!go) break;
+        fac = fac_next;
+      }
     }
   } else {
     if constexpr (Cfg::SPLIT_REGS) ptx::setmaxnreg_dec<Cfg::REG_CONTROL>();
@@ -613,7 +718,7 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
             ok = wait_bar_warp<kRoleMma>(bar(Cfg::B_VFULL + (j - 1) % VST), (uint32_t)(((j - 1) / VST) & 1),
                                          wc, kSiteVFull);
             if (!ok) break;
-            if constexpr (Cfg::RAGGED != 0) clear_tail(j - 1);
+            if constexpr (Cfg::RAGGED == 1 || Cfg::RAGGED == 2) clear_tail(j - 1);
             ptx::tc_fence_after();
 #pragma unroll
             for (int t = 0; t < NQT && ok; ++t)
@@ -632,7 +737,7 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
             ok = wait_bar_warp<kRoleMma>(bar(Cfg::B_VFULL + (j - 1) % VST), (uint32_t)(((j - 1) / VST) & 1),
                                          wc, kSiteVFull);
             if (!ok) break;
-            if constexpr (Cfg::RAGGED != 0) clear_tail(j - 1);
+            if constexpr (Cfg::RAGGED == 1 || Cfg::RAGGED == 2) clear_tail(j - 1);
           }
           ptx::tc_fence_after();
 #pragma unroll

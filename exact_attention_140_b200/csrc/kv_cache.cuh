@@ -16,6 +16,7 @@
 #include <cstdint>
 
 #include "attn_common.cuh"
+#include "e4m3.cuh"
 #include "ptx.cuh"
 
 namespace attn {
@@ -63,17 +64,12 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 // that 2^e, 2^-e and every code * 2^e down to the last subnormal code are exact
 // in bf16; 127 for a row of zeros, 255 for a row that holds an infinity or a
 // NaN (its bits are the largest).
-constexpr uint32_t kExpNaN = 255u;
 __device__ __forceinline__ uint32_t e4m3_row_exponent(uint32_t amax_bits) {
   if (amax_bits >= 0x7F800000u) return kExpNaN;
   if (amax_bits == 0u) return 127u;
   const int x = (int)(amax_bits >> 23) - 126;  // amax = m * 2^x, m in [0.5, 1) (subnormals end at the lower clamp)
   const int e = (amax_bits & 0x7FFFFFu) <= 0x600000u ? x - 9 : x - 8;
   return (uint32_t)((e < -118 ? -118 : e) + 127);
-}
-// The factor 2^(exp - 127) that the byte stands for, NaN for 255.
-__device__ __forceinline__ float exp_factor(uint32_t e) {
-  return __uint_as_float(e == kExpNaN ? 0x7FFFFFFFu : e << 23);
 }
 
 // D / 8 lanes hold one head row, 8 elements (16 bytes) each; a group of lanes
@@ -207,23 +203,6 @@ __global__ void __launch_bounds__(256) head_rows_kernel(const HeadRowsParams p) 
   }
 }
 
-// e4m3 codes to bf16, exactly: the code's bits s eeee mmm placed as the bf16
-// s 0000eeee mmm0000 are the value * 2^-120 (subnormal codes become subnormal
-// bf16), so one product by 2^120 gives the value.  hi: the codes in bytes 1 and
-// 3 of x; lo: those in bytes 0 and 2.
-__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-constexpr uint32_t kBf16x2Pow120 = 0x7B807B80u;  // 2^120 twice
-__device__ __forceinline__ uint32_t e4m3_hi_to_bf16x2(uint32_t x) {
-  return bf16x2_mul(((x >> 4) & 0x07F007F0u) | (x & 0x80008000u), kBf16x2Pow120);
-}
-__device__ __forceinline__ uint32_t e4m3_lo_to_bf16x2(uint32_t x) {
-  return bf16x2_mul(((x << 4) & 0x07F007F0u) | ((x << 8) & 0x80008000u), kBf16x2Pow120);
-}
-
 struct KvReadParams {
   const void *k_pages, *v_pages;
   const unsigned char *k_exp, *v_exp;
@@ -270,12 +249,12 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const KvReadParams p) {
       } else {
         const uint2 q = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const unsigned char*>(src) + row * D) + c);
         const uint32_t e = __ldg((x == 0 ? p.k_exp : p.v_exp) + row + c / (D / 8));
-        const uint32_t m = e == kExpNaN ? 0x7FFF7FFFu : (e << 7) | (e << 23);  // 2^(e - 127) twice
+        const E4m3Factor f = e4m3_factor(e);
         const uint32_t h[4] = {__byte_perm(q.x, 0u, 0x1404), __byte_perm(q.x, 0u, 0x3424), __byte_perm(q.y, 0u, 0x1404),
                                __byte_perm(q.y, 0u, 0x3424)};
         uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = bf16x2_mul(e4m3_hi_to_bf16x2(h[i]), m);
+        for (int i = 0; i < 4; ++i) o[i] = bf16x2_mul(bf16x2_mul(e4m3_hi_bits(h[i]), f.m), f.more);
         w[x] = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }

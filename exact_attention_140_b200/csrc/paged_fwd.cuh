@@ -1,26 +1,41 @@
-// paged_fwd.cuh -- attention of few new tokens over a paged cache, split over
-// windows of keys, and the merge of the windows.
+// paged_fwd.cuh -- attention of few new tokens over a paged cache, shared out
+// along the keys, and the merge of what was shared.
 //
-// One block takes one (sequence, key/value head, tile of packed query rows, key
-// window).  The g query heads of a key/value head share the block: packed row
+// The work is cut into units of 64 or 128 keys of one segment (sequence, tile of packed
+// query rows, key/value head); the grid is what the GPU holds at once and every
+// block takes an equal run of units, so blocks end together whatever the lengths
+// are (windows of fixed size left the longest-working SM at 1.5 times the mean on
+// 32 sequences of up to 8192 keys).  A run may end one segment and begin others;
+// only a segment that is shared between blocks is written as partial rows, at
+// most two per block, and merged by paged_combine_kernel.
+//
+// The g query heads of a key/value head share a segment: packed row
 // r = i * g + h % g of new token i, so a step of decoding reads each cached key
-// once per group.  The block streams its window through a ring of 64-key
-// stages (cp.async, 16 bytes per request, rows gathered through the page table;
-// rows behind the last visible key are filled with zeros, so what the cache
-// holds there cannot reach the products) and runs, per 16 rows x 16 keys of a
-// warp, S = Q K^T, the online softmax and O += P V on the warp-level matrix
-// instruction (m16n8k16).  The kernel is bound by HBM: 16 rows of a decoding
-// group use a tenth of what that instruction delivers, and a 16-row tile wastes
-// far less of the softmax than the 128-row tile of tcgen05.
+// once per group.  A producer warp streams the units through a ring of stages
+// (TMA, one box per page) and runs ahead across segments; four consumer warps run
+// on their own, each on 16 keys of a stage at a time, and meet at a segment's end:
+//   S^T = K Q^T,   the online softmax of every query row (a column),   O^T += V^T P^T
+// on the warp-level matrix instruction (m16n8k16).  The kernel is bound by HBM;
+// what it has to spare are instructions.  With the keys as the 16-row operand a
+// group of up to 8 rows wastes nothing of the product, the accumulator is half
+// as large, and K and V enter as fragments straight from shared memory; only P
+// is transposed (movmatrix).  A row's maximum is exchanged between the lanes only
+// when a lane sees a score past the threshold over the running reference, so
+// most steps exchange nothing.
 //
-// e4m3 cache: codes are expanded to bf16 in registers (exactly), the key's
-// power-of-two scale multiplies its scores in fp32 and the value's its weight
-// before that is rounded to bf16, so nothing but the products' operands is
-// rounded, as with a bf16 cache.
+// Orders that are free are chosen for the loads: which reduction index stands
+// where in a fragment (both operands agree, so a lane's 16-byte load serves two
+// or four instructions), and which of 8 keys is which row (rows r and r + 4 of
+// the 128-byte swizzle share no bank, neighbours do).
 //
-// Which reduction index stands where in a fragment is free as long as both
-// operands agree, so the keys are read with 16-byte shared loads: a lane's 16
-// bytes are the reduction indexes of two (bf16) or four (e4m3) instructions.
+// e4m3 cache: codes become f16 (one conversion instruction per two codes, exact)
+// and the products run in f16.  Queries are scaled per row by a power of two so
+// that they fit f16 exactly (what falls below its normal range is under 2^-38 of
+// the row's largest); the key's power-of-two scale multiplies its scores in fp32.
+// The value's scale joins the exponent of its weight: with t = s + log2(scale),
+// P = 2^(t - m_t) against a reference m_t of t, kept apart from the reference m of
+// s that the row sum uses, and O = 2^(m_t - m) acc / l.  So P is rounded (11 bits)
+// relative to the largest contribution to the output, whatever the scales are.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -31,23 +46,30 @@
 
 namespace attn {
 
-struct PagedParams {
+// The sequences of a paged call.
+struct PagedSeqs {
+  int Tq, n_seqs, max_q, max_kv;
+  const int *cu_q, *kv_lens;  // cu_q may be nullptr: max_q tokens each
+};
+
+struct PagedParams : PagedSeqs {
   const __nv_bfloat16* q;
   long long q_stride;
   __nv_bfloat16* o;  // [Tq, Hq, D]
   float* lse;        // [Hq, Tq] or nullptr
-  int Tq, n_seqs, max_q, Hq, Hkv, group;
-  const int *cu_q, *table, *kv_lens;
-  int table_width, max_kv;
-  const void *k_pages, *v_pages;
+  int Hq, Hkv, group;
+  const int* table;
+  int table_width;
   const unsigned char *k_exp, *v_exp;
   int n_pages, page_shift;
   int causal;
   float sl2;                 // scale * log2(e)
-  int n_windows, window;     // key windows of a sequence of max_kv keys; keys per window (a multiple of 64)
-  int row_tiles;             // tiles of packed rows of a sequence of max_q tokens
-  float *o_part, *lse_part;  // [window][Tq][Hq][D] and [window][Tq][Hq]
+  // workspace: units in front of each sequence and the units of a block, then the
+  // partial rows [2 * blocks][block rows][D] and their LSE [2 * blocks][block rows]
+  long long* base;  // [n_seqs], then the units of a block
+  float *o_part, *lse_part;
   unsigned int* err;
+  unsigned long long timeout_ns;
 };
 
 // The new tokens [q0, q0 + nq) and the cached tokens `len` of sequence s, with
@@ -56,7 +78,7 @@ struct SeqRange {
   int q0, nq, len;
   bool bad;
 };
-__device__ __forceinline__ SeqRange paged_seq(const PagedParams& p, int s) {
+__device__ __forceinline__ SeqRange paged_seq(const PagedSeqs& p, int s) {
   SeqRange r;
   r.bad = false;
   if (p.cu_q == nullptr) {
@@ -80,376 +102,8 @@ __device__ __forceinline__ SeqRange paged_seq(const PagedParams& p, int s) {
   }
   return r;
 }
-
-// D head size, E4M3 cache type, RW: warps along the packed rows (16 each); the
-// other 4 / RW share the keys of a stage, 16 at a time.
-template <int D_, bool E4M3_, int RW_>
-struct PagedCfg {
-  static constexpr int D = D_, RW = RW_, KW = 4 / RW_, TK = 64;
-  static constexpr bool E4M3 = E4M3_;
-  static constexpr int RB = D * (E4M3 ? 1 : 2);  // bytes of a cached row
-  static constexpr int CPR = RB / 16;
-  static constexpr int ROWS = 16 * RW;
-  static constexpr uint32_t TILE = TK * RB, STAGE = 2 * TILE;
-  // stages: about 96 KB of a bf16 ring and 64 KB of an e4m3 one let 2 and 3
-  // blocks share an SM at d = 128
-  static constexpr int NST = STAGE >= 65536 ? 3 : (STAGE >= 32768 ? 3 : 4);
-  static constexpr int MAXW = 2048;               // keys of a window at most
-  static constexpr int OSTR = D + 16;             // floats of a merge row (the padding spreads the banks)
-  static constexpr uint32_t OFF_PAGE = NST * STAGE;                      // page ids of the window
-  static constexpr uint32_t OFF_FAC = OFF_PAGE + 4 * (MAXW / 16 + 4);    // bf16 factors: keys, then values
-  static constexpr uint32_t OFF_ML = OFF_FAC + (E4M3 ? 2 * 2 * MAXW : 0);
-  static constexpr uint32_t SMEM = OFF_ML + 2 * 4 * 4 * 16;
-  static_assert((uint32_t)64 * OSTR * 4 <= NST * STAGE, "the merge rows reuse the ring");
-  static_assert(SMEM <= 227 * 1024, "shared memory per block");
-};
-
-// Byte offset of 16-byte piece c of row r: pieces are permuted within 128
-// bytes so that 8 rows' same piece (ldmatrix) and 2 rows' 4 neighbouring pieces
-// (a quarter warp's 16-byte loads) fall into different banks.
-template <int RB>
-__device__ __forceinline__ uint32_t paged_swz(uint32_t r, uint32_t c) {
-  if constexpr (RB == 64) {
-    return (r >> 1) * 128u + (((r & 1u) << 2) | (c ^ ((r >> 1) & 3u))) * 16u;
-  } else {
-    const uint32_t x = ((r & 1u) << 2) | ((r >> 1) & 3u);
-    return r * RB + ((c & ~7u) | ((c & 7u) ^ x)) * 16u;
-  }
-}
-
-template <class Cfg>
-__global__ void __launch_bounds__(128) paged_fwd_kernel(const PagedParams p) {
-  constexpr int D = Cfg::D, TK = Cfg::TK, KW = Cfg::KW, NST = Cfg::NST, RB = Cfg::RB;
-  constexpr bool E4M3 = Cfg::E4M3;
-  constexpr int KS = D / 16;  // reduction steps of Q K^T
-  extern __shared__ __align__(128) uint8_t psm[];
-  const uint32_t sb = ptx::smem_u32(psm);
-  int* s_page = reinterpret_cast<int*>(psm + Cfg::OFF_PAGE);
-  __nv_bfloat16* s_kf = reinterpret_cast<__nv_bfloat16*>(psm + Cfg::OFF_FAC);
-  __nv_bfloat16* s_vf = s_kf + Cfg::MAXW;
-  float* s_m = reinterpret_cast<float*>(psm + Cfg::OFF_ML);  // [KW][ROWS], 64 in all
-  float* s_l = s_m + 64;
-
-  ptx::grid_dep_launch();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int w = (int)(blockIdx.x % (unsigned)p.n_windows);
-  const int rest = (int)(blockIdx.x / (unsigned)p.n_windows);
-  const int rt = rest % p.row_tiles;
-  const int kh = (rest / p.row_tiles) % p.Hkv;
-  const int s = rest / p.row_tiles / p.Hkv;
-  const SeqRange sr = paged_seq(p, s);
-  if (sr.bad && tid == 0) atomicOr(p.err, kErrIndex);
-  const int g = p.group;
-  const long long rows = (long long)sr.nq * g;
-  const long long row0 = (long long)rt * Cfg::ROWS;
-  if (row0 >= rows) return;
-  const int nwin = sr.len > p.window ? (sr.len + p.window - 1) / p.window : 1;
-  if (w >= nwin) return;
-  const int k0 = w * p.window;
-  int k1 = sr.len - k0 < p.window ? sr.len : k0 + p.window;
-  if (p.causal) {  // the last row of the tile sees the most
-    const long long last = (row0 + Cfg::ROWS < rows ? row0 + Cfg::ROWS : rows) - 1;
-    const long long vis = sr.len - sr.nq + last / g + 1;
-    k1 = vis < k1 ? (int)(vis < k0 ? k0 : vis) : k1;
-  }
-  const int n = k1 - k0 > 0 ? k1 - k0 : 0;  // keys of this block
-  const int n_tiles = (n + TK - 1) / TK;
-
-  // page ids of the window (-1: reads as zeros)
-  const int pg0 = k0 >> p.page_shift;
-  const int npg = n > 0 ? ((k1 - 1) >> p.page_shift) - pg0 + 1 : 0;
-  for (int i = tid; i < npg; i += 128) {
-    int id = pg0 + i < p.table_width ? __ldg(p.table + (long long)s * p.table_width + pg0 + i) : -1;
-    if (id < 0 || id >= p.n_pages) {
-      id = -1;
-      atomicOr(p.err, kErrIndex);
-    }
-    s_page[i] = id;
-  }
-  __syncthreads();
-
-  // cached row of key k0 + i: index into [slots, Hkv], or -1
-  auto cached_row = [&](int i) -> long long {
-    const int key = k0 + i;
-    const int id = s_page[(key >> p.page_shift) - pg0];
-    return id < 0 ? -1 : (((long long)id << p.page_shift) + (key & ((1 << p.page_shift) - 1))) * p.Hkv + kh;
-  };
-  auto load_tile = [&](int j) {
-    const uint32_t kb = sb + (uint32_t)(j % NST) * Cfg::STAGE;
-    constexpr int RPI = 128 / Cfg::CPR;  // rows per round of the block (8, 16, 32 or 4)
-    const int c = tid % Cfg::CPR;
-#pragma unroll
-    for (int i = 0; i < TK / RPI; ++i) {
-      const int r = i * RPI + tid / Cfg::CPR;
-      const int key = j * TK + r;
-      const long long row = key < n ? cached_row(key) : -1;
-      const long long off = row < 0 ? 0 : row * RB + 16 * c;
-      const uint32_t dst = kb + paged_swz<RB>((uint32_t)r, (uint32_t)c);
-      ptx::cp_async16(dst, static_cast<const uint8_t*>(p.k_pages) + off, row >= 0);
-      ptx::cp_async16(dst + Cfg::TILE, static_cast<const uint8_t*>(p.v_pages) + off, row >= 0);
-    }
-  };
-#pragma unroll
-  for (int j = 0; j < NST - 1; ++j) {
-    if (j < n_tiles) load_tile(j);
-    ptx::cp_async_commit();
-  }
-  if constexpr (E4M3) {
-    for (int i = tid; i < n_tiles * TK; i += 128) {
-      const long long row = i < n ? cached_row(i) : -1;
-      const uint32_t ke = row < 0 ? 0u : __ldg(p.k_exp + row), ve = row < 0 ? 0u : __ldg(p.v_exp + row);
-      s_kf[i] = __ushort_as_bfloat16((unsigned short)(ke == kExpNaN ? 0x7FFFu : ke << 7));
-      s_vf[i] = __ushort_as_bfloat16((unsigned short)(ve == kExpNaN ? 0x7FFFu : ve << 7));
-    }
-  }
-
-  // this warp's 16 rows: the lane holds rows gr and gr + 8
-  const int rw = warp % Cfg::RW, kw = warp / Cfg::RW;
-  const int gr = lane >> 2, c = lane & 3;
-  uint32_t qa[KS][4];
-  int lim[2];  // keys (from k0) that the row sees
-#pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
-    const long long r = row0 + rw * 16 + gr + 8 * hf;
-    const int i = (int)(r / g);
-    const bool live = r < rows;
-    const __nv_bfloat16* qr = p.q + (long long)(sr.q0 + i) * p.q_stride + (long long)(kh * g + (int)(r - (long long)i * g)) * D;
-    long long vis = p.causal ? (long long)sr.len - sr.nq + i + 1 - k0 : n;
-    lim[hf] = vis < 0 ? 0 : (vis > n ? n : (int)vis);
-    if constexpr (E4M3) {
-      // step 4 ch + t: reduction indexes 64 ch + 16 c + 4 t + {0, 2 | 1, 3}
-#pragma unroll
-      for (int ch = 0; ch < D / 64; ++ch) {
-        uint4 x[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          x[u] = live ? __ldg(reinterpret_cast<const uint4*>(qr + 64 * ch + 16 * c) + u) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const uint32_t a = t % 2 == 0 ? x[t / 2].x : x[t / 2].z, b = t % 2 == 0 ? x[t / 2].y : x[t / 2].w;
-          qa[4 * ch + t][hf] = __byte_perm(a, b, 0x5410);
-          qa[4 * ch + t][hf + 2] = __byte_perm(a, b, 0x7632);
-        }
-      }
-    } else {
-      // steps 2 ch, 2 ch + 1: reduction indexes 32 ch + 8 c + {0, 1 | 2, 3} and + {4, 5 | 6, 7}
-#pragma unroll
-      for (int ch = 0; ch < D / 32; ++ch) {
-        const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(qr + 32 * ch + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
-        qa[2 * ch][hf] = x.x;
-        qa[2 * ch][hf + 2] = x.y;
-        qa[2 * ch + 1][hf] = x.z;
-        qa[2 * ch + 1][hf + 2] = x.w;
-      }
-    }
-  }
-  float acc[D / 8][4];
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-  for (int j = 0; j < n_tiles; ++j) {
-    ptx::cp_async_wait<NST - 2>();
-    __syncthreads();
-    if (j + NST - 1 < n_tiles) load_tile(j + NST - 1);
-    ptx::cp_async_commit();
-    const uint32_t kb = sb + (uint32_t)(j % NST) * Cfg::STAGE, vb = kb + Cfg::TILE;
-#pragma unroll 1
-    for (int sub = kw; sub < TK / 16; sub += KW) {
-      const int key = j * TK + sub * 16;  // first of 16 keys, from k0
-      if (key >= n) break;
-      // ---- S = Q K^T, two tiles of 8 keys
-      float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const uint32_t r = (uint32_t)(sub * 16 + nt * 8 + gr);
-#pragma unroll
-        for (int ch = 0; ch < Cfg::CPR / 4; ++ch) {
-          uint32_t x[4];
-          ptx::ld_shared_v4(kb + paged_swz<RB>(r, (uint32_t)(4 * ch + c)), x);
-          if constexpr (E4M3) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-              ptx::mma_bf16(sc[nt], qa[4 * ch + t], e4m3_lo_to_bf16x2(x[t]), e4m3_hi_to_bf16x2(x[t]));
-          } else {
-            ptx::mma_bf16(sc[nt], qa[2 * ch], x[0], x[1]);
-            ptx::mma_bf16(sc[nt], qa[2 * ch + 1], x[2], x[3]);
-          }
-        }
-      }
-      // ---- scale, mask, online softmax
-      float vf[2][2];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        float f0 = p.sl2, f1 = p.sl2;
-        vf[nt][0] = vf[nt][1] = 1.f;
-        if constexpr (E4M3) {
-          const uint32_t kf = *reinterpret_cast<const uint32_t*>(s_kf + key + nt * 8 + 2 * c);
-          const uint32_t vv = *reinterpret_cast<const uint32_t*>(s_vf + key + nt * 8 + 2 * c);
-          f0 *= __uint_as_float(kf << 16);
-          f1 *= __uint_as_float(kf & 0xFFFF0000u);
-          vf[nt][0] = __uint_as_float(vv << 16);
-          vf[nt][1] = __uint_as_float(vv & 0xFFFF0000u);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[nt][e] *= (e & 1) ? f1 : f0;
-      }
-      const bool whole = key + 16 <= lim[0] && key + 16 <= lim[1];  // (lim is per lane; masks below are per element)
-      if (!whole) {
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (key + nt * 8 + 2 * c + (e & 1) >= lim[e >> 1]) sc[nt][e] = -INFINITY;
-      }
-      float mx[2];
-      bool grow = false;
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        mx[hf] = fmaxf(fmaxf(sc[0][2 * hf], sc[0][2 * hf + 1]), fmaxf(sc[1][2 * hf], sc[1][2 * hf + 1]));
-        mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 1));
-        mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 2));
-        grow |= mx[hf] > m[hf] + kTau;  // the reference moves only past the threshold
-      }
-      if (__any_sync(0xffffffffu, grow)) {
-        float a[2];
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          a[hf] = 1.f;
-          if (mx[hf] > m[hf] + kTau) {
-            a[hf] = ptx::ex2(m[hf] - mx[hf]);  // 0 from -inf
-            m[hf] = mx[hf];
-            l[hf] *= a[hf];
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][e] *= a[e >> 1];
-      }
-      const float mu[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-      uint32_t pa[4];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        float pr[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          pr[e] = ptx::ex2(sc[nt][e] - mu[e >> 1]);
-          l[e >> 1] += pr[e];
-          if constexpr (E4M3) {
-            // the value's scale, with 2^-8 against the threshold's headroom (put back at the end);
-            // a masked key keeps an exact zero whatever its scale
-            pr[e] = sc[nt][e] == -INFINITY ? 0.f : pr[e] * (vf[nt][e & 1] * 0.00390625f);
-          }
-        }
-        pa[2 * nt] = ptx::pack_bf16x2(pr[0], pr[1]);
-        pa[2 * nt + 1] = ptx::pack_bf16x2(pr[2], pr[3]);
-      }
-      // ---- O += P V
-      const uint32_t vr = (uint32_t)(sub * 16 + (lane & 15));
-#pragma unroll
-      for (int d0 = 0; d0 < Cfg::CPR; d0 += 2) {
-        uint32_t x[4];  // pieces d0, d0 + 1 of keys 0-7 and 8-15
-        ptx::ldmatrix_x4_trans(vb + paged_swz<RB>(vr, (uint32_t)(d0 + (lane >> 4))), x);
-        if constexpr (E4M3) {  // a piece is 16 columns: the even ones and the odd ones
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            ptx::mma_bf16(acc[2 * (d0 + u)], pa, e4m3_lo_to_bf16x2(x[2 * u]), e4m3_lo_to_bf16x2(x[2 * u + 1]));
-            ptx::mma_bf16(acc[2 * (d0 + u) + 1], pa, e4m3_hi_to_bf16x2(x[2 * u]), e4m3_hi_to_bf16x2(x[2 * u + 1]));
-          }
-        } else {
-          ptx::mma_bf16(acc[d0], pa, x[0], x[1]);
-          ptx::mma_bf16(acc[d0 + 1], pa, x[2], x[3]);
-        }
-      }
-    }
-  }
-  ptx::cp_async_wait<0>();
-
-  // ---- merge the key warps: rescale to the common reference, sum, divide
-#pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
-    l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 1);
-    l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 2);
-    if (c == 0) {
-      s_m[kw * Cfg::ROWS + rw * 16 + gr + 8 * hf] = m[hf];
-      s_l[kw * Cfg::ROWS + rw * 16 + gr + 8 * hf] = l[hf];
-    }
-  }
-  __syncthreads();  // (also: every warp is done with the ring)
-  float* so = reinterpret_cast<float*>(psm);
-#pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
-    const int r = rw * 16 + gr + 8 * hf;
-    float mt = s_m[r];
-#pragma unroll
-    for (int k = 1; k < KW; ++k) mt = fmaxf(mt, s_m[k * Cfg::ROWS + r]);
-    const float f = m[hf] == -INFINITY ? 0.f : ptx::ex2(m[hf] - mt);
-    float* row = so + (kw * Cfg::ROWS + r) * Cfg::OSTR;
-    if constexpr (E4M3) {
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-        *reinterpret_cast<float4*>(row + 16 * i + 4 * c) =
-            make_float4(acc[2 * i][2 * hf] * f, acc[2 * i + 1][2 * hf] * f, acc[2 * i][2 * hf + 1] * f,
-                        acc[2 * i + 1][2 * hf + 1] * f);
-    } else {
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        *reinterpret_cast<float2*>(row + 8 * i + 2 * c) = make_float2(acc[i][2 * hf] * f, acc[i][2 * hf + 1] * f);
-    }
-  }
-  __syncthreads();
-  constexpr int PPR = D / 8;  // 8-column pieces of a row
-  for (int i = tid; i < Cfg::ROWS * PPR; i += 128) {
-    const int r = i / PPR, pc = i % PPR;
-    if (row0 + r >= rows) break;
-    float mt = s_m[r];
-#pragma unroll
-    for (int k = 1; k < KW; ++k) mt = fmaxf(mt, s_m[k * Cfg::ROWS + r]);
-    float lt = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < KW; ++k) {
-      const float mk = s_m[k * Cfg::ROWS + r];
-      if (mk != -INFINITY) lt += s_l[k * Cfg::ROWS + r] * ptx::ex2(mk - mt);
-      else lt += s_l[k * Cfg::ROWS + r];  // 0, or NaN from scores that were NaN
-      const float4* src = reinterpret_cast<const float4*>(so + (k * Cfg::ROWS + r) * Cfg::OSTR + 8 * pc);
-      const float4 a = src[0], b = src[1];
-      x[0] += a.x; x[1] += a.y; x[2] += a.z; x[3] += a.w;
-      x[4] += b.x; x[5] += b.y; x[6] += b.z; x[7] += b.w;
-    }
-    const float inv = lt == 0.f ? 0.f : (E4M3 ? 256.f : 1.f) / lt;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = lt == 0.f ? 0.f : x[e] * inv;
-    const float lse = lt == 0.f ? -INFINITY : (mt == -INFINITY ? lt : (mt + log2f(lt)) * 0.6931471805599453f);
-    const long long pr = row0 + r;
-    const int t = sr.q0 + (int)(pr / g), h = kh * g + (int)(pr % g);
-    if (nwin == 1) {
-      reinterpret_cast<uint4*>(p.o + ((long long)t * p.Hq + h) * D)[pc] = pack8(x);
-      if (pc == 0 && p.lse != nullptr) p.lse[(long long)h * p.Tq + t] = lse;
-    } else {
-      const long long at = ((long long)w * p.Tq + t) * p.Hq + h;
-      float4* dst = reinterpret_cast<float4*>(p.o_part + at * D) + 2 * pc;
-      dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-      dst[1] = make_float4(x[4], x[5], x[6], x[7]);
-      if (pc == 0) p.lse_part[at] = lse;
-    }
-  }
-}
-
-// Merge of the windows of each (token, head): one warp per row, as
-// attn_combine_kernel, for packed sequences: row t belongs to the sequence
-// found by bisection, whose length gives its number of windows (rows of a
-// single window are final already).
-template <int D>
-__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p) {
-  ptx::grid_dep_wait();
-  constexpr int PER = D / 32;
-  const long long i = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (i >= (long long)p.Tq * p.Hq) return;
-  const int t = (int)(i / p.Hq), h = (int)(i - (long long)t * p.Hq);
+// The sequence that token t belongs to (-1: none).
+__device__ __forceinline__ int paged_seq_of(const PagedSeqs& p, int t, SeqRange& r) {
   int s;
   if (p.cu_q == nullptr) {
     s = t / p.max_q;
@@ -461,44 +115,840 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p)
     }
     s = lo;
   }
-  if (s >= p.n_seqs) return;
-  const SeqRange sr = paged_seq(p, s);
-  if (t < sr.q0 || t >= sr.q0 + sr.nq || sr.len <= p.window) return;
-  const int S = (sr.len + p.window - 1) / p.window;
-  const long long str = (long long)p.Tq * p.Hq;
-  float mx = -INFINITY;
-  for (int w = lane; w < S; w += 32) mx = fmaxf(mx, p.lse_part[w * str + i]);
+  if (s >= p.n_seqs) return -1;
+  r = paged_seq(p, s);
+  return t >= r.q0 && t < r.q0 + r.nq ? s : -1;
+}
+
+// D head size, E4M3 cache type, NT: tiles of 8 packed rows per warp, RW: warps
+// along the rows; the other 4 / RW share the keys of a stage, 16 at a time.
+template <int D_, bool E4M3_, int NT_, int RW_>
+struct PagedCfg {
+  static constexpr int D = D_, NT = NT_, RW = RW_, KW = 4 / RW_;
+  static constexpr bool E4M3 = E4M3_;
+  // SP: groups of 16 keys a warp takes at once, two where a step is short on
+  // independent work (one tile of rows, many conversions).  TK: keys of a stage,
+  // and of a unit
+  static constexpr int SP = E4M3 && NT == 1 && D <= 128 ? 2 : 1, TK = 64 * SP;
+  static constexpr int RB = D * (E4M3 ? 1 : 2);        // bytes of a cached row
+  static constexpr int CW = RB < 128 ? RB : 128;       // bytes of a box row
+  static constexpr int NCHK = RB / CW;                 // boxes across a row
+  static constexpr int ROWS = 8 * NT * RW;
+  static constexpr uint32_t TILE = TK * RB, STAGE = 2 * TILE;
+  // floats of a merge row (the padding spreads the banks; less of it is what lets
+  // a third block with SP = 2 fit: 98 -> 91 us on 64 sequences of up to 8192 keys)
+  static constexpr int OSTR = D + (SP == 2 ? 4 : 16);
+  static constexpr int MROWS = (KW > 1 ? KW / 2 : 1) * ROWS;
+  // 2 blocks of three 32 KB stages or 3 of two share an SM (two of the largest
+  // stages where the merge rows leave no room for a third)
+  static constexpr int NST = STAGE > 32768 && MROWS > 16 ? 2 : (SP == 2 && STAGE == 32768 ? 2 : (STAGE >= 16384 ? 3 : 4));
+  static constexpr uint32_t OFF_EXP = NST * STAGE;     // exponent bytes of a stage: its keys', its values'
+  static constexpr uint32_t OFF_MRG = OFF_EXP + (E4M3 ? NST * 2 * TK : 0);
+  static constexpr uint32_t OFF_ML = OFF_MRG + MROWS * OSTR * 4;  // [KW][ROWS] of m, l, m_t
+  static constexpr uint32_t OFF_BAR = OFF_ML + 3 * 4 * 64;        // full[NST], empty[NST]
+  static constexpr uint32_t OFF_ABORT = OFF_BAR + 8 * 2 * NST;
+  static constexpr uint32_t OFF_SCAN = OFF_ABORT + 8;             // 5 warp sums, then the first sequence and its units
+  static constexpr uint32_t SMEM = OFF_SCAN + 8 * 8 + 1024;
+  static constexpr int NTHREADS = 160;
+  // blocks that share an SM, by shared memory and by the registers of their
+  // accumulators and queries
+  static constexpr int BY_SMEM = (227 * 1024) / (int)(SMEM + 1024), BY_REGS = NT * D > 128 ? 2 : (NT == 2 ? 3 : 4);
+  static constexpr int BPS = BY_SMEM < 1 ? 1 : (BY_SMEM < BY_REGS ? BY_SMEM : BY_REGS);
+  static_assert(KW * ROWS <= 64, "the exchange of references");
+  static_assert(SMEM <= 227 * 1024, "shared memory per block");
+};
+
+// A sequence's row tiles, and the units of each (row tile, head).
+struct PagedShape {
+  int row_tiles, units;
+};
+__device__ __forceinline__ PagedShape paged_shape(const SeqRange& r, int group, int block_rows, int unit) {
+  PagedShape x;
+  x.row_tiles = (int)(((long long)r.nq * group + block_rows - 1) / block_rows);
+  x.units = r.len > unit ? (r.len + unit - 1) / unit : 1;
+  return x;
+}
+
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
+    paged_fwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const PagedParams p) {
+  constexpr int D = Cfg::D, TK = Cfg::TK, SP = Cfg::SP, KW = Cfg::KW, NST = Cfg::NST, NT = Cfg::NT, CW = Cfg::CW;
+  constexpr bool E4M3 = Cfg::E4M3;
+  constexpr int KS = D / 16;  // reduction steps of K Q^T, 16-row tiles of V^T P^T
+  extern __shared__ uint8_t psm_raw[];
+  const uint32_t raw_u32 = ptx::smem_u32(psm_raw);
+  const uint32_t sb = (raw_u32 + 1023u) & ~1023u;
+  uint8_t* psm = psm_raw + (sb - raw_u32);
+  float* s_m = reinterpret_cast<float*>(psm + Cfg::OFF_ML);  // [KW][ROWS], 64 in all
+  float* s_l = s_m + 64;
+  [[maybe_unused]] float* s_t = s_m + 128;
+  auto full = [&](int st) -> uint32_t { return sb + Cfg::OFF_BAR + 8u * (uint32_t)st; };
+  auto empty = [&](int st) -> uint32_t { return sb + Cfg::OFF_BAR + 8u * (uint32_t)(NST + st); };
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(psm + Cfg::OFF_ABORT);
+  const WaitCtx wc{abort_flag, p.err, p.timeout_ns};
+
+  ptx::grid_dep_launch();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = p.group;
+
+  // ---- this block's run of units: a scan over the sequences, each thread
+  // taking a contiguous share of them
+  long long* s_scan = reinterpret_cast<long long*>(psm + Cfg::OFF_SCAN);
+  const int per = (p.n_seqs + Cfg::NTHREADS - 1) / Cfg::NTHREADS;
+  const int sq0 = tid * per, sq1 = sq0 + per < p.n_seqs ? sq0 + per : p.n_seqs;
+  auto units_of = [&](int s) -> long long {
+    const SeqRange r = paged_seq(p, s);
+    if (r.bad) atomicOr(p.err, kErrIndex);
+    const PagedShape x = paged_shape(r, g, Cfg::ROWS, TK);
+    return (long long)x.row_tiles * p.Hkv * x.units;
+  };
+  long long mine = 0;
+  for (int s = sq0; s < sq1; ++s) mine += units_of(s);
+  long long upto = mine;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) s_scan[warp] = upto;
+  if (tid == 0) {
+    for (int i = 0; i < NST; ++i) {
+      ptx::mbar_init(full(i), E4M3 ? 33 : 1);
+      ptx::mbar_init(empty(i), 4);
+    }
+    *abort_flag = 0u;
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  long long total = 0, front = upto - mine;
+#pragma unroll
+  for (int i = 0; i < Cfg::NTHREADS / 32; ++i) {
+    if (i < warp) front += s_scan[i];
+    total += s_scan[i];
+  }
+  const long long share = (total + gridDim.x - 1) / gridDim.x;
+  const long long u_begin = share * blockIdx.x, u_end = u_begin + share < total ? u_begin + share : total;
+  if (blockIdx.x == 0) {  // for the merge
+    long long at = front;
+    for (int s = sq0; s < sq1; ++s) {
+      p.base[s] = at;
+      at += units_of(s);
+    }
+    if (tid == 0) p.base[p.n_seqs] = share;
+  }
+  if (u_begin >= u_end) return;
+  __syncthreads();  // (the warp sums have been read)
+  if (front <= u_begin && u_begin < front + mine) {
+    long long at = front;
+    int s = sq0;
+    for (;; ++s) {
+      const long long n = units_of(s);
+      if (u_begin < at + n) break;
+      at += n;
+    }
+    s_scan[0] = s;
+    s_scan[1] = at;
+  }
+  __syncthreads();
+
+  // ---- the run as portions: part (from unit `u` on) of a segment (sequence s,
+  // row tile rt, head kh), in order; producer and consumers walk it alike
+  struct Portion {
+    int s, rt, kh;
+    SeqRange sr;
+    PagedShape sh;
+    long long at;    // first unit of the segment
+    long long u;     // first unit of the portion
+    int k0, n;       // its first key, and the keys that some row of the tile sees
+    int n_tiles;
+    bool first, last;  // it holds the segment's first, last unit
+  };
+  auto settle = [&](Portion& x) {
+    const long long stop = x.at + x.sh.units < u_end ? x.at + x.sh.units : u_end;
+    x.first = x.u == x.at;
+    x.last = x.at + x.sh.units <= u_end;
+    x.k0 = (int)(x.u - x.at) * TK;
+    const long long k_stop = (stop - x.at) * TK;
+    int k1 = k_stop < x.sr.len ? (int)k_stop : x.sr.len;
+    if (p.causal) {  // the last row of the tile sees the most
+      const long long rows = (long long)x.sr.nq * g, row0 = (long long)x.rt * Cfg::ROWS;
+      const long long end = (row0 + Cfg::ROWS < rows ? row0 + Cfg::ROWS : rows) - 1;
+      const long long vis = x.sr.len - x.sr.nq + end / g + 1;
+      k1 = vis < k1 ? (int)(vis < 0 ? 0 : vis) : k1;
+    }
+    x.n = k1 > x.k0 ? k1 - x.k0 : 0;
+    x.n_tiles = (x.n + TK - 1) / TK;
+  };
+  auto first_portion = [&]() -> Portion {
+    Portion x;
+    x.s = (int)s_scan[0];
+    x.sr = paged_seq(p, x.s);
+    x.sh = paged_shape(x.sr, g, Cfg::ROWS, TK);
+    const long long seg = (u_begin - s_scan[1]) / x.sh.units;
+    x.rt = (int)(seg / p.Hkv);
+    x.kh = (int)(seg % p.Hkv);
+    x.at = s_scan[1] + seg * x.sh.units;
+    x.u = u_begin;
+    settle(x);
+    return x;
+  };
+  auto next_portion = [&](Portion& x) -> bool {  // false at the end of the run
+    x.at += x.sh.units;
+    if (x.at >= u_end) return false;
+    x.u = x.at;
+    if (++x.kh == p.Hkv) {
+      x.kh = 0;
+      if (++x.rt == x.sh.row_tiles) {
+        x.rt = 0;
+        do {
+          x.sr = paged_seq(p, ++x.s);
+          x.sh = paged_shape(x.sr, g, Cfg::ROWS, TK);
+        } while (x.sh.row_tiles == 0);
+      }
+    }
+    settle(x);
+    return true;
+  };
+
+  if (warp == 4) {
+    // ------------------------------------------------------------ producer
+    // Nothing that was just loaded is looked at in the same round: the table is
+    // read 32 pages at a time, a block of them ahead, and the exponent bytes two
+    // stages ahead (a load's latency is longer than a stage's turn).
+    const int ps = 1 << p.page_shift, br = ps < TK ? ps : TK;  // rows of a box
+    Portion x = first_portion();
+    int issued = 0;  // stages filled
+    bool go = true;
+    do {
+      const int k0 = x.k0, n = x.n, k1 = k0 + n, n_tiles = x.n_tiles, kh = x.kh;
+      const int* table = p.table + (long long)x.s * p.table_width;
+      const int pg0 = k0 >> p.page_shift;
+      auto load_pages = [&](int blk) -> int {  // entries pg0 + 32 blk + lane
+        const long long i = (long long)pg0 + 32ll * blk + lane;
+        return i < p.table_width && (i << p.page_shift) < k1 ? __ldg(table + i) : -1;
+      };
+      int blk = 0, pages = load_pages(0), pages_next = load_pages(1);
+      // the page of key i (from k0), for tiles in block `blk` or the next; n_pages (a
+      // box outside the map: zeros) behind the last key and for a bad page
+      auto page_of = [&](int i) -> int {
+        const int idx = ((k0 + i) >> p.page_shift) - pg0;
+        const int a = __shfl_sync(0xffffffffu, pages, idx & 31), b = __shfl_sync(0xffffffffu, pages_next, idx & 31);
+        const int id = (idx >> 5) == blk ? a : b;
+        if (i >= n) return p.n_pages;
+        if (id >= 0 && id < p.n_pages) return id;
+        atomicOr(p.err, kErrIndex);
+        return p.n_pages;
+      };
+      struct Exps { uint32_t k[TK / 32], v[TK / 32]; };  // bytes of keys lane + 32 u of a tile
+      auto exps_of = [&](int j) -> Exps {
+        Exps r;
+#pragma unroll
+        for (int u = 0; u < TK / 32; ++u) {
+          const int i = j * TK + lane + 32 * u, id = page_of(i);
+          const long long at = (((long long)id << p.page_shift) + ((k0 + i) & (ps - 1))) * p.Hkv + kh;
+          const bool there = id < p.n_pages;
+          r.k[u] = there ? __ldg(p.k_exp + at) : 127u;
+          r.v[u] = there ? __ldg(p.v_exp + at) : 127u;
+        }
+        return r;
+      };
+      [[maybe_unused]] Exps ex[2];
+      if constexpr (E4M3) {
+        ex[0] = exps_of(0);
+        ex[1] = exps_of(1);
+      }
+      for (int j0 = 0; go && j0 < n_tiles; j0 += 2) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int j = j0 + u;
+          if (!go || j >= n_tiles) continue;
+          const int b = ((k0 + j * TK) >> p.page_shift) - pg0;
+          if ((b >> 5) != blk) {
+            blk = b >> 5;
+            pages = pages_next;
+            pages_next = load_pages(blk + 1);
+          }
+          const int page = page_of(j * TK + (lane < TK / br ? lane * br : 0));
+          const int st = issued % NST;
+          if (issued >= NST &&
+              !wait_bar_warp<kRoleProducer>(empty(st), (uint32_t)((issued / NST - 1) & 1), wc, kSiteKEmpty)) {
+            go = false;
+            continue;
+          }
+          const uint32_t kb = sb + (uint32_t)st * Cfg::STAGE;
+          if (lane == 0) ptx::mbar_arrive_expect_tx(full(st), Cfg::STAGE);
+          __syncwarp();
+          if (lane < TK / br) {
+            const int r0 = ps < TK ? 0 : (k0 + j * TK) & (ps - 1);
+#pragma unroll
+            for (int ch = 0; ch < Cfg::NCHK; ++ch) {
+              const uint32_t dst = kb + ch * (TK * CW) + lane * br * CW;
+              constexpr int BOXE = CW / (E4M3 ? 1 : 2);
+              ptx::tma_load_4d(dst, &tmK, full(st), ch * BOXE, kh, r0, page);
+              ptx::tma_load_4d(dst + Cfg::TILE, &tmV, full(st), ch * BOXE, kh, r0, page);
+            }
+          }
+          ++issued;
+          if constexpr (E4M3) {
+            uint8_t* se = psm + Cfg::OFF_EXP + st * 2 * TK;
+#pragma unroll
+            for (int e = 0; e < TK / 32; ++e) {
+              se[32 * e + lane] = (uint8_t)ex[u].k[e];
+              se[TK + 32 * e + lane] = (uint8_t)ex[u].v[e];
+            }
+            ptx::mbar_arrive(full(st));
+            ex[u] = exps_of(j + 2);
+          }
+        }
+      }
+    } while (go && next_portion(x));
+    // every copy has to land before the block may end
+#pragma unroll
+    for (int i = 0; i < NST; ++i) {
+      const int f = (issued - i + NST - 1) / NST;  // fills of stage i
+      if (f > 0) wait_bar_drain<kRoleProducer>(full(i), (uint32_t)((f - 1) & 1), wc, kSiteKFull);
+    }
+    __syncthreads();
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int rw = warp % Cfg::RW, kw = warp / Cfg::RW;
+  const int gr = lane >> 2, c = lane & 3;
+  // key of row i of a fragment, among 8
+  auto key_of = [](int i) -> int { return CW == 128 ? ((i >> 1) & 3) | ((i & 1) << 2) : i; };
+  // byte offset of 16-byte piece pc of row r in a tile, as TMA lays it out
+  auto at = [](int r, int pc) -> uint32_t {
+    constexpr int PPR = CW / 16;
+    const int x = CW == 128 ? r & 7 : (r >> 1) & 3;
+    return (uint32_t)((pc / PPR) * (TK * CW) + r * CW + (((pc % PPR) ^ x) << 4));
+  };
+  Portion x = first_portion();
+  int it = 0;  // stages consumed
+  bool ok = true;
+  do {
+    const long long rows = (long long)x.sr.nq * g, row0 = (long long)x.rt * Cfg::ROWS;
+    const int n = x.n;
+    uint32_t qb[KS][NT][2];
+    float rs[NT][2];   // what a raw score of rows 2c, 2c + 1 is multiplied by
+    int lim[NT][2];    // keys (from k0) that they see
+    int lim_min = n;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const long long r = row0 + rw * 8 * NT + nt * 8 + gr;
+      const int i = (int)(r / g);
+      const bool live = r < rows;
+      const __nv_bfloat16* qr = p.q + (long long)(x.sr.q0 + i) * p.q_stride + (long long)(x.kh * g + (int)(r - (long long)i * g)) * D;
+      float scale = p.sl2;
+      if constexpr (E4M3) {
+        // step 4 ch + t: reduction indexes 64 ch + 16 c + 4 t + {0, 1 | 2, 3}
+        uint4 qx[D / 64][2];
+        uint32_t top = 0u;  // largest magnitude (bits of bf16, in the upper half of a word)
+#pragma unroll
+        for (int ch = 0; ch < D / 64; ++ch)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            qx[ch][u] = live ? __ldg(reinterpret_cast<const uint4*>(qr + 64 * ch + 16 * c) + u) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t y[4] = {qx[ch][u].x, qx[ch][u].y, qx[ch][u].z, qx[ch][u].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              top = max(top, y[e] & 0x7FFF0000u);
+              top = max(top, (y[e] << 16) & 0x7FFF0000u);
+            }
+          }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // the largest lands in [2^14, 2^15)
+        int sh = 141 - (int)(top >> 23);
+        sh = top == 0u ? 0 : (sh > 126 ? 126 : sh);
+        const float up = __uint_as_float((uint32_t)(sh + 127) << 23);
+        scale *= __uint_as_float((uint32_t)(127 - sh) << 23);
+#pragma unroll
+        for (int ch = 0; ch < D / 64; ++ch)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t a = t % 2 == 0 ? qx[ch][t / 2].x : qx[ch][t / 2].z, b = t % 2 == 0 ? qx[ch][t / 2].y : qx[ch][t / 2].w;
+            qb[4 * ch + t][nt][0] = ptx::pack_f16x2(__uint_as_float(a << 16) * up, __uint_as_float(a & 0xFFFF0000u) * up);
+            qb[4 * ch + t][nt][1] = ptx::pack_f16x2(__uint_as_float(b << 16) * up, __uint_as_float(b & 0xFFFF0000u) * up);
+          }
+      } else {
+        // steps 2 ch, 2 ch + 1: reduction indexes 32 ch + 8 c + {0, 1 | 2, 3} and + {4, 5 | 6, 7}
+#pragma unroll
+        for (int ch = 0; ch < D / 32; ++ch) {
+          const uint4 y = live ? __ldg(reinterpret_cast<const uint4*>(qr + 32 * ch + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
+          qb[2 * ch][nt][0] = y.x;
+          qb[2 * ch][nt][1] = y.y;
+          qb[2 * ch + 1][nt][0] = y.z;
+          qb[2 * ch + 1][nt][1] = y.w;
+        }
+      }
+      const long long vis = p.causal ? (long long)x.sr.len - x.sr.nq + i + 1 - x.k0 : n;
+      const int my_lim = !live ? n : (vis < 0 ? 0 : (vis > n ? n : (int)vis));
+      lim_min = min(lim_min, my_lim);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {  // from the lanes that hold rows 2c, 2c + 1 as their own
+        rs[nt][e] = __shfl_sync(0xffffffffu, scale, (2 * c + e) * 4);
+        lim[nt][e] = __shfl_sync(0xffffffffu, my_lim, (2 * c + e) * 4);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, o));
+
+    // thresholds, log2 units: the references move when a score passes them by
+    // TAU; P stays within 2^8, or for e4m3 within 2^15 with a reference 7 below the
+    // maximum (f16 then resolves 2^-31 of the largest contribution)
+    constexpr float kUp = E4M3 ? 7.f : 0.f;
+    float acc[NT][KS][4];
+    float m[NT][2], l[NT][2], mt[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[nt][i][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[nt][e] = mt[nt][e] = -INFINITY;
+        l[nt][e] = 0.f;
+      }
+    }
+
+    for (int j = 0; j < x.n_tiles; ++j, ++it) {
+      const int st = it % NST;
+      ok = wait_bar_warp<kRoleSoftmax>(full(st), (uint32_t)((it / NST) & 1), wc, kSiteKFull);
+      if (!ok) break;
+      const uint32_t kb = sb + (uint32_t)st * Cfg::STAGE, vb = kb + Cfg::TILE;
+#pragma unroll 1
+      for (int sub = kw * SP; sub < TK / 16; sub += KW * SP) {
+        const int key = j * TK + sub * 16;  // first of 16 * SP keys, from k0
+        if (key >= n) break;
+        const int kr = sub * 16 + key_of(gr);
+        // ---- S^T = K Q^T
+        float sc[SP][NT][4];
+#pragma unroll
+        for (int q = 0; q < SP; ++q)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[q][nt][e] = 0.f;
+#pragma unroll
+        for (int ch = 0; ch < Cfg::RB / 64; ++ch) {
+#pragma unroll
+          for (int q = 0; q < SP; ++q) {
+            uint32_t fx[4], fy[4];
+            ptx::ld_shared_v4(kb + at(kr + 16 * q, 4 * ch + c), fx);
+            ptx::ld_shared_v4(kb + at(kr + 16 * q + 8, 4 * ch + c), fy);
+            if constexpr (E4M3) {
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                uint32_t a[4];
+                ptx::e4m3x4_to_f16x4(fx[t], a[0], a[2]);
+                ptx::e4m3x4_to_f16x4(fy[t], a[1], a[3]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) ptx::mma_f16(sc[q][nt], a, qb[4 * ch + t][nt][0], qb[4 * ch + t][nt][1]);
+              }
+            } else {
+              const uint32_t a0[4] = {fx[0], fy[0], fx[1], fy[1]}, a1[4] = {fx[2], fy[2], fx[3], fy[3]};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                ptx::mma_bf16(sc[q][nt], a0, qb[2 * ch][nt][0], qb[2 * ch][nt][1]);
+                ptx::mma_bf16(sc[q][nt], a1, qb[2 * ch + 1][nt][0], qb[2 * ch + 1][nt][1]);
+              }
+            }
+          }
+        }
+        // ---- scale, mask, online softmax (element e: key gr + 8 (e >> 1), row 2c + (e & 1))
+        const bool whole = key + 16 * SP <= lim_min;  // every row of the warp sees all the keys
+        bool grow = false;
+        [[maybe_unused]] float tt[SP][NT][4];
+        float sx[NT][2], tx[NT][2];  // this lane's largest
+#pragma unroll
+        for (int q = 0; q < SP; ++q) {
+          float kf[2] = {1.f, 1.f}, kv[2] = {0.f, 0.f};
+          if constexpr (E4M3) {
+            const uint8_t* se = psm + Cfg::OFF_EXP + st * 2 * TK + kr + 16 * q;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t ke = se[8 * h], ve = se[TK + 8 * h];
+              kf[h] = __uint_as_float(ke == kExpNaN ? 0x7FFFFFFFu : ke << 23);
+              kv[h] = ve == kExpNaN ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float(0x4B000000u | ve) - 8388735.f;
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              sc[q][nt][e] *= E4M3 ? rs[nt][e & 1] * kf[e >> 1] : rs[nt][e & 1];
+              if constexpr (E4M3) tt[q][nt][e] = sc[q][nt][e] + kv[e >> 1];
+            }
+            if (!whole) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (key + 16 * q + key_of(gr) + 8 * (e >> 1) >= lim[nt][e & 1]) {
+                  sc[q][nt][e] = -INFINITY;
+                  if constexpr (E4M3) tt[q][nt][e] = -INFINITY;
+                }
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float a = fmaxf(sc[q][nt][e], sc[q][nt][e + 2]), b = E4M3 ? fmaxf(tt[q][nt][e], tt[q][nt][e + 2]) : 0.f;
+              sx[nt][e] = q == 0 ? a : fmaxf(sx[nt][e], a);
+              tx[nt][e] = q == 0 ? b : fmaxf(tx[nt][e], b);
+            }
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            grow |= sx[nt][e] > m[nt][e] + kTau;
+            if constexpr (E4M3) grow |= tx[nt][e] > mt[nt][e] + (kTau + kUp);
+          }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float a = sx[nt][e], b = tx[nt][e];
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) {
+                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+                if constexpr (E4M3) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+              }
+              float fa = 1.f, fb = 1.f;
+              if (a > m[nt][e]) {
+                fa = ptx::ex2(m[nt][e] - a);  // 0 from -inf
+                m[nt][e] = a;
+                l[nt][e] *= fa;
+              }
+              if constexpr (E4M3) {
+                if (b - kUp > mt[nt][e]) {
+                  fb = ptx::ex2(mt[nt][e] - (b - kUp));
+                  mt[nt][e] = b - kUp;
+                }
+              } else {
+                fb = fa;
+              }
+#pragma unroll
+              for (int i = 0; i < KS; ++i) {
+                acc[nt][i][e] *= fb;
+                acc[nt][i][e + 2] *= fb;
+              }
+            }
+        }
+        uint32_t pb[SP][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float mu[2], mv[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            mu[e] = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+            mv[e] = mt[nt][e] == -INFINITY ? 0.f : mt[nt][e];
+          }
+#pragma unroll
+          for (int q = 0; q < SP; ++q) {
+            float pr[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              pr[e] = ptx::ex2(sc[q][nt][e] - mu[e & 1]);
+              l[nt][e & 1] += pr[e];
+              if constexpr (E4M3) pr[e] = ptx::ex2(tt[q][nt][e] - mv[e & 1]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              pb[q][nt][h] = ptx::movmatrix_trans(E4M3 ? ptx::pack_f16x2(pr[2 * h], pr[2 * h + 1])
+                                                       : ptx::pack_bf16x2(pr[2 * h], pr[2 * h + 1]));
+          }
+        }
+        // ---- O^T += V^T P^T; the last keys' tile: what stands behind them must
+        // not be multiplied, not even by zero
+        const bool tail = key + 16 * SP > n;
+        uint32_t live[SP][2];
+        if (tail) {
+#pragma unroll
+          for (int q = 0; q < SP; ++q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int k = key + 16 * q + 8 * h;
+              live[q][h] = (k + key_of(2 * c) < n ? 0xFFFFu : 0u) | (k + key_of(2 * c + 1) < n ? 0xFFFF0000u : 0u);
+            }
+        }
+        if constexpr (E4M3) {
+          // matrices: keys 0-7 and 8-15 of piece d0, the same of piece d0 + 1
+          const int vr = sub * 16 + 8 * ((lane >> 3) & 1) + key_of(lane & 7);
+#pragma unroll
+          for (int d0 = 0; d0 < KS; d0 += 2) {
+#pragma unroll
+            for (int q = 0; q < SP; ++q) {
+              uint32_t fv[4];
+              ptx::ldmatrix_x4_trans(vb + at(vr + 16 * q, d0 + (lane >> 4)), fv);
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                // a word: columns 2 gr, 2 gr + 1 of two keys; the even column is row gr, the odd one row gr + 8
+                uint32_t a[4], lo, hi;
+                if (tail) {
+                  fv[2 * u] &= live[q][0];
+                  fv[2 * u + 1] &= live[q][1];
+                }
+                ptx::e4m3x4_to_f16x4(fv[2 * u], lo, hi);
+                a[0] = __byte_perm(lo, hi, 0x5410);
+                a[1] = __byte_perm(lo, hi, 0x7632);
+                ptx::e4m3x4_to_f16x4(fv[2 * u + 1], lo, hi);
+                a[2] = __byte_perm(lo, hi, 0x5410);
+                a[3] = __byte_perm(lo, hi, 0x7632);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) ptx::mma_f16(acc[nt][d0 + u], a, pb[q][nt][0], pb[q][nt][1]);
+              }
+            }
+          }
+        } else {
+          // matrices: keys 0-7 of pieces 2 i and 2 i + 1, then keys 8-15 of them
+          const int vr = sub * 16 + 8 * (lane >> 4) + key_of(lane & 7);
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+#pragma unroll
+            for (int q = 0; q < SP; ++q) {
+              uint32_t fv[4];
+              ptx::ldmatrix_x4_trans(vb + at(vr + 16 * q, 2 * i + ((lane >> 3) & 1)), fv);
+              if (tail) {
+                fv[0] &= live[q][0];
+                fv[1] &= live[q][0];
+                fv[2] &= live[q][1];
+                fv[3] &= live[q][1];
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) ptx::mma_bf16(acc[nt][i], fv, pb[q][nt][0], pb[q][nt][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(empty(st));
+    }
+    if (!ok) break;
+
+    // ---- merge the key warps: rescale to the common references, sum, divide.
+    // (A warp whose wait ran out goes through the same barriers; all leave together
+    // below.)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], o);
+        if (gr == 0) {
+          const int r = kw * Cfg::ROWS + rw * 8 * NT + nt * 8 + 2 * c + e;
+          s_m[r] = m[nt][e];
+          s_l[r] = l[nt][e];
+          if constexpr (E4M3) s_t[r] = mt[nt][e];
+        }
+      }
+    if (KW > 1) ptx::bar_sync(1, 128);
+    // acc stands against the reference `ref` of its warp
+    const float* s_ref = E4M3 ? s_t : s_m;
+    float* so = reinterpret_cast<float*>(psm + Cfg::OFF_MRG);
+    auto columns = [&](float* row, int i, float a, float b) {  // this lane's two columns of 16-column piece i
+      if constexpr (E4M3) {
+        *reinterpret_cast<float2*>(row + 16 * i + 2 * gr) = make_float2(a, b);
+      } else {
+        row[16 * i + gr] = a;
+        row[16 * i + gr + 8] = b;
+      }
+    };
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (KW == 1) break;
+        const int r = rw * 8 * NT + nt * 8 + 2 * c + e;
+        float top = s_ref[r];
+#pragma unroll
+        for (int k = 1; k < KW; ++k) top = fmaxf(top, s_ref[k * Cfg::ROWS + r]);
+        const float own = E4M3 ? mt[nt][e] : m[nt][e];
+        const float f = own == -INFINITY ? 1.f : ptx::ex2(own - top);  // (without a reference acc is 0, or NaN)
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          acc[nt][i][e] *= f;
+          acc[nt][i][e + 2] *= f;
+        }
+      }
+#pragma unroll
+    for (int half = KW / 2; half >= 1; half /= 2) {  // the upper half hands its sums to the lower
+      if (kw >= half && kw < 2 * half) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+              columns(so + ((kw - half) * Cfg::ROWS + rw * 8 * NT + nt * 8 + 2 * c + e) * Cfg::OSTR, i, acc[nt][i][e],
+                      acc[nt][i][e + 2]);
+      }
+      ptx::bar_sync(1, 128);
+      if (kw < half) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float* row = so + (kw * Cfg::ROWS + rw * 8 * NT + nt * 8 + 2 * c + e) * Cfg::OSTR;
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+              acc[nt][i][e] += row[16 * i + (E4M3 ? 2 * gr : gr)];
+              acc[nt][i][e + 2] += row[16 * i + (E4M3 ? 2 * gr + 1 : gr + 8)];
+            }
+          }
+      }
+      if (half > 1) ptx::bar_sync(1, 128);
+    }
+    if (kw == 0) {
+      __syncwarp();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = rw * 8 * NT + nt * 8 + 2 * c + e;
+          float mx = s_m[r], tx = s_ref[r];
+#pragma unroll
+          for (int k = 1; k < KW; ++k) {
+            mx = fmaxf(mx, s_m[k * Cfg::ROWS + r]);
+            tx = fmaxf(tx, s_ref[k * Cfg::ROWS + r]);
+          }
+          float lt = 0.f;
+#pragma unroll
+          for (int k = 0; k < KW; ++k) {
+            const float mk = s_m[k * Cfg::ROWS + r], lk = s_l[k * Cfg::ROWS + r];
+            lt += mk == -INFINITY ? lk : lk * ptx::ex2(mk - mx);  // (without a reference l is 0, or NaN)
+          }
+          float inv = lt == 0.f ? 0.f : 1.f / lt;
+          if constexpr (E4M3) {
+            if (tx != -INFINITY && mx != -INFINITY) inv *= ptx::ex2(tx - mx);
+          }
+          float* row = so + r * Cfg::OSTR;
+#pragma unroll
+          for (int i = 0; i < KS; ++i)
+            columns(row, i, lt == 0.f ? 0.f : acc[nt][i][e] * inv, lt == 0.f ? 0.f : acc[nt][i][e + 2] * inv);
+          // (each lane group writes the same value; the padding behind the row holds it)
+          row[D] = lt == 0.f ? -INFINITY : (mx == -INFINITY ? lt : (mx + log2f(lt)) * 0.6931471805599453f);
+        }
+    }
+    ptx::bar_sync(1, 128);
+    constexpr int PPR = D / 8;  // 8-column pieces of a row
+    for (int i = tid; i < Cfg::ROWS * PPR; i += 128) {
+      const int r = i / PPR, pc = i % PPR;
+      if (row0 + r >= rows) break;
+      const float* row = so + r * Cfg::OSTR;
+      const float4 a = reinterpret_cast<const float4*>(row)[2 * pc], b = reinterpret_cast<const float4*>(row)[2 * pc + 1];
+      if (x.first && x.last) {
+        const long long pr = row0 + r;
+        const int t = x.sr.q0 + (int)(pr / g), h = x.kh * g + (int)(pr % g);
+        const float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        reinterpret_cast<uint4*>(p.o + ((long long)t * p.Hq + h) * D)[pc] = pack8(y);
+        if (pc == 0 && p.lse != nullptr) p.lse[(long long)h * p.Tq + t] = row[D];
+      } else {
+        const long long to = (2ll * blockIdx.x + (x.last ? 0 : 1)) * Cfg::ROWS + r;
+        float4* dst = reinterpret_cast<float4*>(p.o_part + to * D) + 2 * pc;
+        dst[0] = a;
+        dst[1] = b;
+        if (pc == 0) p.lse_part[to] = row[D];
+      }
+    }
+    if (!ptx::bar_red_and(1, 128, ok)) break;  // (then the merge rows and references are free again)
+  } while (next_portion(x));
+  __syncthreads();
+}
+
+// One output row from S partial rows, by a warp: part w is row slot(w) of o_part
+// (fp32, normalised by its own sum) with its LSE (natural log) in lse_part.
+//   LSE = ln sum_w exp(LSE_w),   O = sum_w exp(LSE_w - LSE) O_w
+// (parts without a visible key have LSE_w = -inf and weigh nothing.)  Bound by the
+// latency of a few reads from L2: eight parts' rows are requested together.
+template <int D, class Slot>
+__device__ __forceinline__ void merge_parts(const float* o_part, const float* lse_part, int S, Slot slot, int lane,
+                                            __nv_bfloat16* o, float* lse) {
+  constexpr int PER = D / 32;
+  float mx = -INFINITY;
+  for (int w = lane; w < S; w += 32) mx = fmaxf(mx, __ldcg(lse_part + slot(w)));
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
   const float mu = mx == -INFINITY ? 0.f : mx;
   float acc[PER], wsum = 0.f;
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
   for (int w0 = 0; w0 < S; w0 += 32) {
-    const float wl = w0 + lane < S ? expf(p.lse_part[(w0 + lane) * str + i] - mu) : 0.f;
+    const float wl = w0 + lane < S ? expf(__ldcg(lse_part + slot(w0 + lane)) - mu) : 0.f;
     const int n = S - w0 < 32 ? S - w0 : 32;
     for (int j0 = 0; j0 < n; j0 += 8) {
-      float wt[8], x[8][PER];
+      float wt[8], y[8][PER];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         wt[u] = __shfl_sync(0xffffffffu, wl, (j0 + u) & 31);
         const bool live = j0 + u < n && wt[u] != 0.f;  // uniform across the warp
 #pragma unroll
-        for (int e = 0; e < PER; ++e) x[u][e] = live ? p.o_part[((w0 + j0 + u) * str + i) * D + 32 * e + lane] : 0.f;
+        for (int e = 0; e < PER; ++e) y[u][e] = live ? __ldcg(o_part + slot(w0 + j0 + u) * D + 32 * e + lane) : 0.f;
         if (!live) wt[u] = 0.f;
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         wsum += wt[u];
 #pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] = fmaf(wt[u], x[u][e], acc[e]);
+        for (int e = 0; e < PER; ++e) acc[e] = fmaf(wt[u], y[u][e], acc[e]);
       }
     }
   }
   const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
 #pragma unroll
-  for (int e = 0; e < PER; ++e) p.o[i * D + 32 * e + lane] = __float2bfloat16_rn(acc[e] * inv);
-  if (lane == 0 && p.lse != nullptr) p.lse[(long long)h * p.Tq + t] = wsum == 0.f ? -INFINITY : mu + logf(wsum);
+  for (int e = 0; e < PER; ++e) o[32 * e + lane] = __float2bfloat16_rn(acc[e] * inv);
+  if (lane == 0 && lse != nullptr) *lse = wsum == 0.f ? -INFINITY : mu + logf(wsum);
+}
+
+// Merge of the segments that several blocks shared: one warp per (token, head).
+// The row's segment lies in the units [a, b), so in the blocks a / share ..
+// (b - 1) / share; each wrote a partial row (slot 1: its segment goes on in the
+// next block, slot 0: it ends here), and one block alone wrote the result itself.
+template <int D>
+__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p, int block_rows, int unit) {
+  ptx::grid_dep_wait();
+  const long long i = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (i >= (long long)p.Tq * p.Hq) return;
+  const int t = (int)(i / p.Hq), h = (int)(i - (long long)t * p.Hq);
+  SeqRange sr;
+  const int s = paged_seq_of(p, t, sr);
+  if (s < 0) return;
+  const int g = p.group, units = paged_shape(sr, g, block_rows, unit).units;
+  const long long pr = (long long)(t - sr.q0) * g + h % g;
+  const int r = (int)(pr % block_rows);
+  const long long share = __ldcg(p.base + p.n_seqs);
+  const long long a = __ldcg(p.base + s) + ((pr / block_rows) * p.Hkv + h / g) * units;
+  const long long i0 = a / share, i1 = (a + units - 1) / share;
+  if (i0 == i1) return;
+  const int S = (int)(i1 - i0 + 1);
+  merge_parts<D>(p.o_part, p.lse_part, S,
+                 [&](int w) -> long long { return (2 * (i0 + w) + (w == S - 1 ? 0 : 1)) * block_rows + r; },
+                 threadIdx.x & 31, p.o + i * D, p.lse != nullptr ? p.lse + (long long)h * p.Tq + t : nullptr);
+}
+
+// Merge of the key windows of the tcgen05 kernel's items, parts
+// [window][Tq][Hq]; a sequence of one window is final already.
+struct WindowParams : PagedSeqs {
+  __nv_bfloat16* o;
+  float* lse;
+  int Hq, window;
+  const float *o_part, *lse_part;
+};
+template <int D>
+__global__ void __launch_bounds__(256) window_combine_kernel(const WindowParams p) {
+  ptx::grid_dep_wait();
+  const long long i = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (i >= (long long)p.Tq * p.Hq) return;
+  const int t = (int)(i / p.Hq), h = (int)(i - (long long)t * p.Hq);
+  SeqRange sr;
+  if (paged_seq_of(p, t, sr) < 0 || sr.len <= p.window) return;
+  const long long all = (long long)p.Tq * p.Hq;
+  merge_parts<D>(p.o_part, p.lse_part, (sr.len + p.window - 1) / p.window,
+                 [&](int w) -> long long { return w * all + i; }, threadIdx.x & 31, p.o + i * D,
+                 p.lse != nullptr ? p.lse + (long long)h * p.Tq + t : nullptr);
 }
 
 }  // namespace attn

@@ -93,110 +93,159 @@ int launch_kv_read(const KvReadParams& p, cudaStream_t s) {
 }
 
 // ---------------------------------------------------------------- paged attention
-// Windows of a paged call.
+// How a paged call runs.  Few rows per sequence: paged_fwd_kernel, `size` its
+// block configuration, `blocks` its grid.  More (items > 0): the tcgen05 kernel
+// over listed items, each sequence's keys cut into n_windows windows where the
+// items are too few for the GPU.
 struct PagedPlan {
-  int rw, row_tiles, window, n_windows;
-  long long items;  // > 0: tcgen05 kernel over this many listed items at most
+  int size, block_rows, unit, blocks;
+  long long items;
+  int window, n_windows;
 };
 long long ragged_max_items(long long Tq, long long n_seqs, int Hq, int Hkv, int d);
 int ragged_block_rows(int d);
 int ragged_rows_per_token(int Hq, int Hkv);
 long long ragged_plan_bytes(long long items);
 
-PagedPlan paged_plan(const attn_kv_cache_t* c, int Tq, int n_seqs, int max_q, int Hq, int max_kv, int n_splits) {
+constexpr int kSms = 148;  // SMs of a B200: the grids and their workspace go by it
+// Rows of a block: one tile of 8 rows a warp, then two where the accumulators fit
+// (d = 256: one), then more warps along the rows.
+constexpr int kPagedSizes = 4;
+int paged_block_rows(int d, int size) { return size == 0 ? 8 : (d == 256 ? 8 : 16) << (size - 1); }
+template <int D, bool E4M3, int SIZE>
+using PagedCfgOf = PagedCfg<D, E4M3, (SIZE == 0 || D == 256) ? 1 : 2, SIZE <= 1 ? 1 : (SIZE == 2 ? 2 : 4)>;
+struct PagedGeometry {
+  int unit, blocks_per_sm;  // keys of a unit; blocks that share an SM
+};
+template <int D, bool E4M3>
+PagedGeometry paged_geometry(int size) {
+  constexpr PagedGeometry b[kPagedSizes] = {{PagedCfgOf<D, E4M3, 0>::TK, PagedCfgOf<D, E4M3, 0>::BPS},
+                                            {PagedCfgOf<D, E4M3, 1>::TK, PagedCfgOf<D, E4M3, 1>::BPS},
+                                            {PagedCfgOf<D, E4M3, 2>::TK, PagedCfgOf<D, E4M3, 2>::BPS},
+                                            {PagedCfgOf<D, E4M3, 3>::TK, PagedCfgOf<D, E4M3, 3>::BPS}};
+  return b[size];
+}
+PagedGeometry paged_geometry(int d, bool e4m3, int size) {
+  switch (d) {
+    case 64: return e4m3 ? paged_geometry<64, true>(size) : paged_geometry<64, false>(size);
+    case 128: return e4m3 ? paged_geometry<128, true>(size) : paged_geometry<128, false>(size);
+    default: return e4m3 ? paged_geometry<256, true>(size) : paged_geometry<256, false>(size);
+  }
+}
+
+PagedPlan paged_plan(const attn_kv_cache_t* c, int Tq, int n_seqs, int max_q, int Hq, int max_kv) {
   PagedPlan pl = {};
   const int Hkv = c->Hkv;
   const long long rows = (long long)max_q * (Hq / Hkv);
-  if (rows > 64 && c->dtype == ATTN_BF16 && c->n_pages > 0) {
+  if (rows > 64 && c->n_pages > 0) {
     pl.items = ragged_max_items(Tq, n_seqs, Hq, Hkv, c->d);
     const int g = ragged_rows_per_token(Hq, Hkv);
-    long long want = n_splits;
-    if (n_splits <= 0) {  // about two blocks per SM, windows of 512 keys at least
-      const long long blocks = ((long long)Tq * g / ragged_block_rows(c->d) + (n_seqs + 1) / 2) * (g > 1 ? Hkv : Hq);
-      want = (2ll * 148 + blocks - 1) / (blocks > 0 ? blocks : 1);
-      const long long cap = max_kv / 512;
-      want = want > cap ? cap : want;
-      want = want < 1 ? 1 : want;
-    }
+    // about two blocks per SM, windows of 512 keys at least
+    const long long blocks = ((long long)Tq * g / ragged_block_rows(c->d) + (n_seqs + 1) / 2) * (g > 1 ? Hkv : Hq);
+    long long want = (2ll * kSms + blocks - 1) / (blocks > 0 ? blocks : 1);
+    const long long cap = max_kv / 512;
+    want = want > cap ? cap : want;
+    want = want < 1 ? 1 : want;
     const long long w = (((long long)max_kv + want - 1) / want + 127) / 128 * 128;
     pl.window = (int)(w < 128 ? 128 : w);
     pl.n_windows = max_kv > pl.window ? (int)(((long long)max_kv + pl.window - 1) / pl.window) : 1;
     return pl;
   }
-  pl.rw = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
-  pl.row_tiles = (int)((rows + 16 * pl.rw - 1) / (16 * pl.rw));
-  long long w;
-  if (n_splits > 0) {
-    w = ((long long)max_kv + n_splits - 1) / n_splits;
-  } else {
-    // enough blocks to fill the GPU a few times over, windows of 128 keys at least
-    const long long units = (long long)n_seqs * Hkv * pl.row_tiles;
-    w = units * max_kv / (8 * 148);
-    w = w < 128 ? 128 : w;
-  }
-  w = (w + 63) / 64 * 64;
-  pl.window = (int)(w < 64 ? 64 : (w > 2048 ? 2048 : w));
-  pl.n_windows = max_kv > pl.window ? (max_kv + pl.window - 1) / pl.window : 1;
+  while (pl.size < kPagedSizes - 1 && paged_block_rows(c->d, pl.size) < rows) ++pl.size;
+  pl.block_rows = paged_block_rows(c->d, pl.size);
+  const PagedGeometry ge = paged_geometry(c->d, c->dtype == ATTN_FP8_E4M3, pl.size);
+  pl.unit = ge.unit;
+  const long long units = (long long)n_seqs * ((rows + pl.block_rows - 1) / pl.block_rows) * Hkv *
+                          (max_kv > pl.unit ? ((long long)max_kv + pl.unit - 1) / pl.unit : 1);
+  const long long most = (long long)kSms * ge.blocks_per_sm;
+  pl.blocks = (int)(units < most ? units : most);
   return pl;
 }
-// Workspace: the item list, then the windows' partial rows and their LSE.
-long long paged_list_bytes(const PagedPlan& pl) { return pl.items > 0 ? ragged_plan_bytes(pl.items) : 0; }
-long long paged_o_bytes(const PagedPlan& pl, long long Tq, long long Hq, long long d) {
-  return (pl.n_windows * Tq * Hq * d * 4 + 255) / 256 * 256;
-}
-long long paged_bytes(const PagedPlan& pl, long long Tq, long long Hq, long long d) {
-  return paged_list_bytes(pl) + (pl.n_windows > 1 ? paged_o_bytes(pl, Tq, Hq, d) + pl.n_windows * Tq * Hq * 4 : 0);
+// Workspace.  paged_fwd_kernel: a long long per sequence and one, the partial
+// rows, their LSE.  tcgen05: the item list, the windows' partial rows, their LSE.
+struct PagedSpace {
+  long long head, o, lse;  // bytes of each
+  long long all() const { return head + o + lse; }
+};
+PagedSpace paged_space(const PagedPlan& pl, long long Tq, long long n_seqs, long long Hq, long long d) {
+  auto round = [](long long b) { return (b + 255) / 256 * 256; };
+  PagedSpace s = {};
+  if (pl.items > 0) {
+    s.head = ragged_plan_bytes(pl.items);
+    if (pl.n_windows > 1) {
+      s.o = round(pl.n_windows * Tq * Hq * d * 4);
+      s.lse = round(pl.n_windows * Tq * Hq * 4);
+    }
+    return s;
+  }
+  s.head = round((n_seqs + 1) * 8);
+  s.o = 2ll * pl.blocks * pl.block_rows * d * 4;
+  s.lse = round(2ll * pl.blocks * pl.block_rows * 4);
+  return s;
 }
 
 template <class Cfg>
-int launch_paged_cfg(const PagedParams& p, DeviceState* st, cudaStream_t s) {
+int launch_paged_cfg(const PagedParams& p, int blocks, const attn_kv_cache_t* c, DeviceState* st, cudaStream_t s) {
   static std::atomic<unsigned> attr_set[kMaxDevices];
   int rc = set_smem_once(paged_fwd_kernel<Cfg>, (int)Cfg::SMEM, attr_set, st);
   if (rc != ATTN_OK) return rc;
-  const long long blocks = (long long)p.n_windows * p.row_tiles * p.Hkv * p.n_seqs;
-  if (blocks > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;
-  ATTN_LOGF("attn: paged_fwd_kernel<%d, %s, RW=%d> grid=(%lld) block=128 smem=%u seqs=%d max_q=%d Hq=%d Hkv=%d windows=%d x %d\n",
-            Cfg::D, Cfg::E4M3 ? "e4m3" : "bf16", Cfg::RW, blocks, (unsigned)Cfg::SMEM, p.n_seqs, p.max_q, p.Hq, p.Hkv,
-            p.n_windows, p.window);
-  paged_fwd_kernel<Cfg><<<(unsigned)blocks, 128, Cfg::SMEM, s>>>(p);
+  CUtensorMap tk, tv;
+  std::memset(&tk, 0, sizeof(tk));
+  std::memset(&tv, 0, sizeof(tv));
+  if (p.max_kv > 0) {  // (without a key the maps are never used)
+    const auto encode = Cfg::E4M3 ? encode_pages_e4m3 : encode_pages;
+    const int rows = c->page_size < Cfg::TK ? c->page_size : Cfg::TK;
+    if (encode(&tk, c->k_pages, c->n_pages, c->page_size, c->Hkv, c->d, rows) != ATTN_OK ||
+        encode(&tv, c->v_pages, c->n_pages, c->page_size, c->Hkv, c->d, rows) != ATTN_OK)
+      return ATTN_ERR_CUDA;
+  }
+  ATTN_LOGF("attn: paged_fwd_kernel<%d, %s, NT=%d RW=%d> grid=(%d) block=%d smem=%u seqs=%d max_q=%d Hq=%d Hkv=%d\n",
+            Cfg::D, Cfg::E4M3 ? "e4m3" : "bf16", Cfg::NT, Cfg::RW, blocks, Cfg::NTHREADS, (unsigned)Cfg::SMEM, p.n_seqs,
+            p.max_q, p.Hq, p.Hkv);
+  paged_fwd_kernel<Cfg><<<(unsigned)blocks, Cfg::NTHREADS, Cfg::SMEM, s>>>(tk, tv, p);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 template <int D, bool E4M3>
-int launch_paged_rw(const PagedParams& p, int rw, DeviceState* st, cudaStream_t s) {
-  switch (rw) {
-    case 1: return launch_paged_cfg<PagedCfg<D, E4M3, 1>>(p, st, s);
-    case 2: return launch_paged_cfg<PagedCfg<D, E4M3, 2>>(p, st, s);
-    default: return launch_paged_cfg<PagedCfg<D, E4M3, 4>>(p, st, s);
+int launch_paged_size(const PagedParams& p, const PagedPlan& pl, const attn_kv_cache_t* c, DeviceState* st, cudaStream_t s) {
+  switch (pl.size) {
+    case 0: return launch_paged_cfg<PagedCfgOf<D, E4M3, 0>>(p, pl.blocks, c, st, s);
+    case 1: return launch_paged_cfg<PagedCfgOf<D, E4M3, 1>>(p, pl.blocks, c, st, s);
+    case 2: return launch_paged_cfg<PagedCfgOf<D, E4M3, 2>>(p, pl.blocks, c, st, s);
+    default: return launch_paged_cfg<PagedCfgOf<D, E4M3, 3>>(p, pl.blocks, c, st, s);
   }
 }
-template <int D>
-int launch_paged_combine(const PagedParams& p, cudaStream_t s) {
-  const long long blocks = ((long long)p.Tq * p.Hq + 7) / 8;
+// A kernel that is launched while the one before it in the stream still runs and
+// waits for that one's results on the device, so its launch overlaps it.
+template <class... Args>
+int launch_dependent(void (*kernel)(Args...), long long blocks, int threads, size_t smem, cudaStream_t s, Args... args) {
   if (blocks > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;
-  // launched while the attention kernel still runs; it waits for that kernel's
-  // results on the device, so only its launch overlaps
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  ATTN_LOGF("attn: paged_combine_kernel<%d> grid=(%lld) block=256 Tq=%d Hq=%d windows=%d\n", D, blocks, p.Tq, p.Hq,
-            p.n_windows);
-  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D>, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 template <int D>
-int launch_paged(const PagedParams& p, bool e4m3, int rw, DeviceState* st, cudaStream_t s) {
-  const int rc = e4m3 ? launch_paged_rw<D, true>(p, rw, st, s) : launch_paged_rw<D, false>(p, rw, st, s);
-  if (rc != ATTN_OK || p.n_windows == 1) return rc;
-  return launch_paged_combine<D>(p, s);
+int launch_paged(const PagedParams& p, const PagedPlan& pl, const attn_kv_cache_t* c, DeviceState* st, cudaStream_t s) {
+  const int rc = c->dtype == ATTN_FP8_E4M3 ? launch_paged_size<D, true>(p, pl, c, st, s)
+                                           : launch_paged_size<D, false>(p, pl, c, st, s);
+  if (rc != ATTN_OK || p.max_kv <= pl.unit) return rc;  // (a segment of one unit is never shared)
+  const long long blocks = ((long long)p.Tq * p.Hq + 7) / 8;
+  ATTN_LOGF("attn: paged_combine_kernel<%d> grid=(%lld) block=256 Tq=%d Hq=%d\n", D, blocks, p.Tq, p.Hq);
+  return launch_dependent(paged_combine_kernel<D>, blocks, 256, 0, s, p, pl.block_rows, pl.unit);
 }
 
 // ---------------------------------------------------------------- packed sequences on tcgen05
-// The long-range configurations over packed sequences (1) or a paged cache (2);
+// The long-range configurations over packed sequences (1) or a paged cache (2
+// bf16, 3 e4m3), all exponentials on the hardware unit: the software share
+// would lose a NaN score, and over packed sequences it gains nothing (1715
+// against 1728 us at 8192 tokens causal, 331 against 320 us on 512-token chunks);
 // the heads of a group are always stacked where the group divides the tile: a
 // block then covers fewer tokens, which wastes less of a causal block's diagonal
 // and of a short sequence, and a key tile is read once per group.
@@ -254,8 +303,9 @@ int launch_ragged(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
   } else {
     const attn_kv_cache_t* ch = c.cache;
     const int rows = ch->page_size < Cfg::BN ? ch->page_size : Cfg::BN;
-    if (encode_pages(&tk, ch->k_pages, ch->n_pages, ch->page_size, ch->Hkv, ch->d, rows) != ATTN_OK ||
-        encode_pages(&tv, ch->v_pages, ch->n_pages, ch->page_size, ch->Hkv, ch->d, rows) != ATTN_OK)
+    const auto encode = Cfg::KV8 ? encode_pages_e4m3 : encode_pages;
+    if (encode(&tk, ch->k_pages, ch->n_pages, ch->page_size, ch->Hkv, ch->d, rows) != ATTN_OK ||
+        encode(&tv, ch->v_pages, ch->n_pages, ch->page_size, ch->Hkv, ch->d, rows) != ATTN_OK)
       return ATTN_ERR_CUDA;
   }
   PlanParams pp;
@@ -308,24 +358,17 @@ int launch_ragged(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
   p.rg.table_width = c.table_width;
   p.rg.page_shift = c.cache != nullptr ? page_shift(c.cache) : 0;
   p.rg.n_pages = c.cache != nullptr ? c.cache->n_pages : 0;
+  p.rg.k_exp = c.cache != nullptr ? c.cache->k_exp : nullptr;
+  p.rg.v_exp = c.cache != nullptr ? c.cache->v_exp : nullptr;
   const dim3 grid((unsigned)blocks);
   if (log_on()) {
     char extra[96];
     std::snprintf(extra, sizeof extra, " packed sequences%s windows=%d x %d pack=%d band=%d",
-                  Cfg::RAGGED == 2 ? " (paged)" : "", c.n_windows, c.window, g, p.band);
+                  Cfg::RAGGED == 1 ? "" : (Cfg::KV8 ? " (paged e4m3)" : " (paged)"), c.n_windows, c.window, g, p.band);
     log_launch<Cfg>("attn_fwd_kernel", grid, c.n_seqs, c.Hq, c.Hkv, c.Tq, c.Tk, extra);
   }
-  cudaLaunchAttribute at;  // the launch overlaps the plan kernel, which the kernel waits for
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(Cfg::NTHREADS);
-  cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
-  cfg.stream = s;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_fwd_kernel<Cfg>, tq, tk, tv, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  // (the launch overlaps the plan kernel, which the kernel waits for)
+  return launch_dependent(attn_fwd_kernel<Cfg>, blocks, Cfg::NTHREADS, Cfg::SMEM_BYTES, s, tq, tk, tv, (const FwdParams)p);
 }
 template <int R>
 int launch_ragged_d(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
@@ -559,19 +602,20 @@ int attn_fwd_varlen(const void* q, const void* k, const void* v, void* o, float*
   return launch_ragged_d<1>(c, st, static_cast<cudaStream_t>(stream));
 }
 
-long long attn_fwd_paged_workspace_bytes(const attn_kv_cache_t* cache, int Tq, int n_seqs, int max_q, int Hq, int max_kv,
-                                         int n_splits) {
+long long attn_fwd_paged_workspace_bytes(const attn_kv_cache_t* cache, int Tq, int n_seqs, int max_q, int Hq,
+                                         int max_kv) {
   const int rc = check_paged_sizes(cache, Tq, n_seqs, max_q, Hq, max_kv);
   if (rc == -1) return 0;
   if (rc != ATTN_OK) return -1;
-  const PagedPlan pl = paged_plan(cache, Tq, n_seqs, max_q, Hq, max_kv, n_splits);
-  return paged_bytes(pl, Tq, Hq, cache->d);
+  if (cache->n_pages == 0) max_kv = 0;
+  const PagedPlan pl = paged_plan(cache, Tq, n_seqs, max_q, Hq, max_kv);
+  return paged_space(pl, Tq, n_seqs, Hq, cache->d).all();
 }
 
 int attn_fwd_paged(const void* q, const attn_kv_cache_t* cache, void* o, float* lse, int Tq, int n_seqs, int max_q,
                    const int* cu_q, const int* table, int table_width, const int* kv_lens, int max_kv, int Hq,
-                   long long q_stride, int causal, float scale, int n_splits, void* workspace,
-                   long long workspace_bytes, void* stream) {
+                   long long q_stride, int causal, float scale, void* workspace, long long workspace_bytes,
+                   void* stream) {
   int rc = check_paged_sizes(cache, Tq, n_seqs, max_q, Hq, max_kv);
   if (rc > 0) return rc;
   if ((causal != 0 && causal != 1) || !std::isfinite(scale) || table_width < 0) return ATTN_ERR_INVALID_ARG;
@@ -584,47 +628,25 @@ int attn_fwd_paged(const void* q, const attn_kv_cache_t* cache, void* o, float* 
   if (!aligned16(o) || ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(cu_q) |
                          reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(kv_lens)) & 3u) != 0)
     return ATTN_ERR_MISALIGNED;
-  const PagedPlan pl = paged_plan(cache, Tq, n_seqs, max_q, Hq, max_kv, n_splits);
-  const long long need = paged_bytes(pl, Tq, Hq, d);
-  if (need > 0) {
-    if (workspace == nullptr || workspace_bytes < need) return ATTN_ERR_INVALID_ARG;
-    if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
-  }
+  if (cache->n_pages == 0) max_kv = 0;  // there is nothing to read
+  const PagedPlan pl = paged_plan(cache, Tq, n_seqs, max_q, Hq, max_kv);
+  const PagedSpace sp = paged_space(pl, Tq, n_seqs, Hq, d);
+  if (workspace == nullptr || workspace_bytes < sp.all()) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
   int dev = 0;
   DeviceState* st = nullptr;
   if ((rc = device_state(&dev, &st)) != ATTN_OK) return rc;
-  PagedParams p;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.q_stride = q_stride;
-  p.o = static_cast<__nv_bfloat16*>(o);
-  p.lse = lse;
-  p.Tq = Tq;
-  p.n_seqs = n_seqs;
-  p.max_q = max_q;
-  p.Hq = Hq;
-  p.Hkv = cache->Hkv;
-  p.group = Hq / cache->Hkv;
-  p.cu_q = cu_q;
-  p.table = table;
-  p.kv_lens = kv_lens;
-  p.table_width = table_width;
-  p.max_kv = max_kv;
-  p.k_pages = cache->k_pages;
-  p.v_pages = cache->v_pages;
-  p.k_exp = cache->k_exp;
-  p.v_exp = cache->v_exp;
-  p.n_pages = cache->n_pages;
-  p.page_shift = page_shift(cache);
-  p.causal = causal;
-  p.sl2 = scale * 1.4426950408889634f;
-  p.n_windows = pl.n_windows;
-  p.window = pl.window;
-  p.row_tiles = pl.row_tiles;
-  char* parts = static_cast<char*>(workspace) + paged_list_bytes(pl);
-  p.o_part = pl.n_windows > 1 ? reinterpret_cast<float*>(parts) : nullptr;
-  p.lse_part = pl.n_windows > 1 ? reinterpret_cast<float*>(parts + paged_o_bytes(pl, Tq, Hq, d)) : nullptr;
-  p.err = st->err;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  float* o_part = sp.o > 0 ? reinterpret_cast<float*>(ws + sp.head) : nullptr;
+  float* lse_part = sp.o > 0 ? reinterpret_cast<float*>(ws + sp.head + sp.o) : nullptr;
+  PagedSeqs seqs;
+  seqs.Tq = Tq;
+  seqs.n_seqs = n_seqs;
+  seqs.max_q = max_q;
+  seqs.max_kv = max_kv;
+  seqs.cu_q = cu_q;
+  seqs.kv_lens = kv_lens;
   if (pl.items > 0) {
     RaggedCall c = {};
     c.q = q;
@@ -649,22 +671,54 @@ int attn_fwd_paged(const void* q, const attn_kv_cache_t* cache, void* o, float* 
     c.scale = scale;
     c.n_windows = pl.n_windows;
     c.window = pl.window;
-    c.o_part = p.o_part;
-    c.lse_part = p.lse_part;
+    c.o_part = o_part;
+    c.lse_part = lse_part;
     c.plan = static_cast<int*>(workspace);
-    rc = launch_ragged_d<2>(c, st, s);
+    rc = cache->dtype == ATTN_FP8_E4M3 ? launch_ragged_d<3>(c, st, s) : launch_ragged_d<2>(c, st, s);
     if (rc != ATTN_OK || pl.n_windows == 1) return rc;
+    WindowParams wp;
+    static_cast<PagedSeqs&>(wp) = seqs;
+    wp.o = static_cast<__nv_bfloat16*>(o);
+    wp.lse = lse;
+    wp.Hq = Hq;
+    wp.window = pl.window;
+    wp.o_part = o_part;
+    wp.lse_part = lse_part;
+    const long long blocks = ((long long)Tq * Hq + 7) / 8;
+    ATTN_LOGF("attn: window_combine_kernel<%d> grid=(%lld) block=256 Tq=%d Hq=%d windows=%d\n", d, blocks, Tq, Hq,
+              pl.n_windows);
     switch (d) {
-      case 64: return launch_paged_combine<64>(p, s);
-      case 128: return launch_paged_combine<128>(p, s);
-      default: return launch_paged_combine<256>(p, s);
+      case 64: return launch_dependent(window_combine_kernel<64>, blocks, 256, 0, s, (const WindowParams)wp);
+      case 128: return launch_dependent(window_combine_kernel<128>, blocks, 256, 0, s, (const WindowParams)wp);
+      default: return launch_dependent(window_combine_kernel<256>, blocks, 256, 0, s, (const WindowParams)wp);
     }
   }
-  const bool e4m3 = cache->dtype == ATTN_FP8_E4M3;
+  PagedParams p;
+  static_cast<PagedSeqs&>(p) = seqs;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_stride = q_stride;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.Hq = Hq;
+  p.Hkv = cache->Hkv;
+  p.group = Hq / cache->Hkv;
+  p.table = table;
+  p.table_width = table_width;
+  p.k_exp = cache->k_exp;
+  p.v_exp = cache->v_exp;
+  p.n_pages = cache->n_pages;
+  p.page_shift = page_shift(cache);
+  p.causal = causal;
+  p.sl2 = scale * 1.4426950408889634f;
+  p.base = static_cast<long long*>(workspace);
+  p.o_part = o_part;
+  p.lse_part = lse_part;
+  p.err = st->err;
+  p.timeout_ns = timeout_ns();
   switch (d) {
-    case 64: return launch_paged<64>(p, e4m3, pl.rw, st, s);
-    case 128: return launch_paged<128>(p, e4m3, pl.rw, st, s);
-    default: return launch_paged<256>(p, e4m3, pl.rw, st, s);
+    case 64: return launch_paged<64>(p, pl, cache, st, s);
+    case 128: return launch_paged<128>(p, pl, cache, st, s);
+    default: return launch_paged<256>(p, pl, cache, st, s);
   }
 }
 

@@ -510,16 +510,17 @@ int attn_fwd_varlen(const void *q, const void *k, const void *v, void *o, float 
  *              j <= i + kv_len - n_new (causal = 1), or every key (causal = 0)
  *   max_kv     an upper bound of kv_lens, 0 .. table_width * page_size; only
  *              steers how the work is split, but keys behind it are not read
- *   n_splits   key windows per sequence, <= 0: chosen from the sizes
  *   workspace  as attn_fwd_varlen, attn_fwd_paged_workspace_bytes(...) bytes
+ * How a sequence's keys are shared out between blocks depends on the other
+ * sequences of the call, and with it the last bits of the result.
  * The cache's memory behind a sequence's last token may hold anything, NaN too.
  */
 long long attn_fwd_paged_workspace_bytes(const attn_kv_cache_t *cache, int Tq, int n_seqs, int max_q, int Hq,
-                                         int max_kv, int n_splits);
+                                         int max_kv);
 int attn_fwd_paged(const void *q, const attn_kv_cache_t *cache, void *o, float *lse, int Tq, int n_seqs, int max_q,
                    const int *cu_q, const int *table, int table_width, const int *kv_lens, int max_kv, int Hq,
-                   long long q_stride, int causal, float scale, int n_splits, void *workspace,
-                   long long workspace_bytes, void *stream);
+                   long long q_stride, int causal, float scale, void *workspace, long long workspace_bytes,
+                   void *stream);
 
 /*
  * Which kernel attn_fwd / attn_fwd_fp8 launch for a key range of Nk keys at

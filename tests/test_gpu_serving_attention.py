@@ -146,20 +146,21 @@ PAGED = [  # Hq, Hkv, d, new tokens, cached tokens, page size
 ]
 
 
-@pytest.mark.parametrize("n_splits", [0, 1, 3])
+@pytest.mark.parametrize("wide", [0, 1])
 @pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("case", range(len(PAGED)))
-def test_paged(case, e4m3, causal, n_splits):
-    """Every unwritten slot of the cache holds NaN, and unused table entries hold no page."""
+def test_paged(case, e4m3, causal, wide):
+    """Every unwritten slot of the cache holds NaN, and unused table entries hold no page.  wide: a table with
+    room for far longer sequences, which the sizes that steer the split are taken from."""
     torch, ea, su = setup()
     Hq, Hkv, d, new, lens, page = PAGED[case]
-    cache, table, ks, vs = su.make_cache(ea, lens, page, Hkv, d, e4m3, seed=case)
+    cache, table, ks, vs = su.make_cache(ea, lens, page, Hkv, d, e4m3, seed=case, width=20000 // page if wide else None)
     q = rand(torch, sum(new), Hq, d, seed=case + 50)
     o = torch.full(q.shape, 9.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((Hq, sum(new)), 9.0, device="cuda")
     ea.attention_paged(q, cache, table, su.i32(*lens), cu_q=su.starts(new), max_q=max(new), causal=causal,
-                       n_splits=n_splits, o=o, lse=lse)
+                       o=o, lse=lse)
     su.no_device_error(ea)
     a = 0
     for n, k, v in zip(new, ks, vs):
@@ -226,7 +227,7 @@ def test_paged_large_scores():
     cache, table, ks, vs = su.make_cache(ea, [600], 16, 2, 128, False, seed=9)
     for n in (1, 200):
         q = (rand(torch, n, 8, 128, seed=n).float() * 30).to(torch.bfloat16)
-        o, lse = ea.attention_paged(q, cache, table, su.i32(600), n_splits=2)
+        o, lse = ea.attention_paged(q, cache, table, su.i32(600))
         su.check_attention(o, lse, su.attention(q, ks[0], vs[0], True, 1 / math.sqrt(128)), 128)
 
 
@@ -291,12 +292,12 @@ def test_graph_replayed_with_other_lengths():
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
         for _ in range(2):
-            ea.attention_paged(q, cache, table, lens, cu_q=cu, max_q=1, n_splits=2)
+            ea.attention_paged(q, cache, table, lens, cu_q=cu, max_q=1)
             ea.attention_varlen(x[:, :2], x[:, 2:3], x[:, 3:], cq, cq, causal=True)
     torch.cuda.current_stream().wait_stream(side)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        o, lse = ea.attention_paged(q, cache, table, lens, cu_q=cu, max_q=1, n_splits=2)
+        o, lse = ea.attention_paged(q, cache, table, lens, cu_q=cu, max_q=1)
         o2, l2 = ea.attention_varlen(x[:, :2], x[:, 2:3], x[:, 3:], cq, cq, causal=True)
     for new, c in (([300, 300, 300], [0, 100, 260]), ([7, 160, 299], [0, 259, 260]), ([1, 0, 64], [0, 30, 200])):
         lens.copy_(su.i32(*new))
@@ -316,7 +317,7 @@ def test_calls_on_two_streams():
     lens = [900, 1200, 40]
     cache, table, ks, vs = su.make_cache(ea, lens, 16, 2, 128, False, seed=4)
     q = rand(torch, 3, 8, 128, seed=5)
-    want = ea.attention_paged(q, cache, table, su.i32(*lens), n_splits=3)
+    want = ea.attention_paged(q, cache, table, su.i32(*lens))
     x = rand(torch, 500, 6, 128, seed=6)
     cu = su.i32(0, 130, 500)
     want2 = ea.attention_varlen(x[:, :4], x[:, 4:5], x[:, 5:], cu, cu, causal=True)
@@ -325,7 +326,7 @@ def test_calls_on_two_streams():
     s = [torch.cuda.Stream() for _ in range(2)]
     got = []
     for i in range(12):
-        got.append(ea.attention_paged(q, cache, table, kv, n_splits=3, stream=s[i % 2]))
+        got.append(ea.attention_paged(q, cache, table, kv, stream=s[i % 2]))
         got.append(ea.attention_varlen(x[:, :4], x[:, 4:5], x[:, 5:], cu, cu, causal=True, stream=s[1 - i % 2]))
     torch.cuda.synchronize()
     su.no_device_error(ea)

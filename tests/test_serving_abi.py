@@ -117,11 +117,11 @@ def test_varlen_workspace():
 
 def paged(c=None, **kw):
     a = dict(q=P, o=P, lse=P, Tq=4, n=2, max_q=2, cq=P, table=P, width=4, lens=P, max_kv=64, Hq=4, qs=512, causal=1,
-             scale=0.1, splits=0, ws=None, wsb=0)
+             scale=0.1, ws=P, wsb=1 << 30)
     a.update(kw)
     return ea.attn_fwd_paged(a["q"], cache() if c is None else c, a["o"], a["lse"], a["Tq"], a["n"], a["max_q"], a["cq"],
                              a["table"], a["width"], a["lens"], a["max_kv"], a["Hq"], a["qs"], a["causal"], a["scale"],
-                             a["splits"], a["ws"], a["wsb"], stream=0, raise_on_error=False)
+                             a["ws"], a["wsb"], stream=0, raise_on_error=False)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -130,8 +130,7 @@ def paged(c=None, **kw):
     (dict(causal=3), INVALID), (dict(scale=math.inf), INVALID), (dict(cq=None, Tq=3), INVALID),
     (dict(lens=None), INVALID), (dict(o=None), INVALID), (dict(table=None), INVALID), (dict(q=None), INVALID),
     (dict(q=P + 8), MISALIGNED), (dict(qs=516), MISALIGNED), (dict(o=P + 8), MISALIGNED), (dict(table=P + 2), MISALIGNED),
-    (dict(width=400, max_kv=6400, splits=4), INVALID), (dict(width=400, max_kv=6400, splits=4, ws=P, wsb=100), INVALID),
-    (dict(width=400, max_kv=6400, splits=4, ws=P + 4, wsb=1 << 30), MISALIGNED),
+    (dict(ws=None), INVALID), (dict(wsb=100), INVALID), (dict(ws=P + 4), MISALIGNED),
     (dict(Tq=0), OK), (dict(n=0), OK), (dict(Hq=0), OK)])
 def test_paged_refusals(kw, status):
     assert paged(**kw) == status
@@ -141,10 +140,13 @@ def test_paged_workspace():
     f = ea.attn_fwd_paged_workspace_bytes
     c = cache(Hkv=8)
     assert f(c, 0, 1, 1, 32, 64) == 0 and f(c, 4, 4, 1, 33, 64) == -1 and f(c, 4, 4, 5, 32, 64) == -1
-    assert f(c, 4, 4, 1, 32, 64, 1) == 0
-    # three windows of 64 keys: fp32 rows and their LSE
-    assert f(c, 4, 4, 1, 32, 192, 3) == 3 * 4 * 32 * 128 * 4 + 3 * 4 * 32 * 4
-    assert f(c, 64, 64, 1, 32, 1 << 17) > 0  # long contexts always split
+    # a count per sequence, and two partial blocks of 8 rows for each of the 4 * 8 * 3 units of 64 keys
+    assert f(c, 4, 4, 1, 32, 192) == 256 + 2 * 96 * 8 * 128 * 4 + 2 * 96 * 8 * 4
+    assert f(c, 64, 64, 1, 32, 1 << 17) == f(c, 64, 64, 1, 32, 1 << 20)  # the grid is bounded by the GPU
+    # 300 tokens of 4 stacked heads: the item list; with long contexts windows join it
+    items = (300 * 4 + 255) // 256
+    assert f(c, 300, 1, 300, 32, 500) == (32 + 32 * items + 255) // 256 * 256
+    assert f(c, 300, 1, 300, 32, 1 << 16) > 300 * 32 * 128 * 4 * 2
 
 
 def freqs(*a, **kw):
