@@ -97,12 +97,15 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
     const int2 i1 = __ldcg(reinterpret_cast<const int2*>(p.rg.plan) + 6 + 4 * item);
     hy = bi * p.band + within % bsz;
     b = 0;
-    seq = i0.x;
-    qb = i0.y;
-    q_base = i0.z;
-    nq = i0.w;
-    k_base = i1.x;
-    nk_all = i1.y;
+    // (a shuffle from lane 0 shows the compiler that the warp agrees on them, so
+    // that loops and descriptors stay in uniform registers)
+    auto uni = [](int v) -> int { return __shfl_sync(0xffffffffu, v, 0); };
+    seq = uni(i0.x);
+    qb = uni(i0.y);
+    q_base = uni(i0.z);
+    nq = uni(i0.w);
+    k_base = uni(i1.x);
+    nk_all = uni(i1.y);
     if (split > 0 && split * p.kv_chunk >= nk_all) return;  // no such window
   } else if (p.band > 0) {
     // longest-first within bands of (batch, head) pairs: a band's K/V stay in
