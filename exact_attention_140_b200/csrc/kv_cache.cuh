@@ -22,16 +22,15 @@
 namespace attn {
 
 struct HeadRowsParams {
+  long long T;
   // inputs: token t of x at x + t * stride (elements), heads contiguous
   const __nv_bfloat16 *q, *k, *v;
   long long q_stride, k_stride, v_stride;
   int Hq, Hkv;
-  bool has_v;
   // dense outputs (rows of q always; rows of k unless they go to the cache)
   __nv_bfloat16 *q_out, *k_out;
   long long q_out_stride, k_out_stride;
-  // cache (to_cache): pages as [n_slots, Hkv, d]
-  bool to_cache;
+  // cache modes: pages as [n_slots, Hkv, d]
   const long long* slots;
   long long n_slots;
   void *k_pages, *v_pages;
@@ -72,131 +71,143 @@ __device__ __forceinline__ uint32_t e4m3_row_exponent(uint32_t amax_bits) {
   return (uint32_t)((e < -118 ? -118 : e) + 127);
 }
 
-// D / 8 lanes hold one head row, 8 elements (16 bytes) each; a group of lanes
-// takes UNROLL rows of one token, loaded together.  A block holds the rows
-// [blockIdx.y * rows per block, ...) of one token; the cosines and sines of
-// the token's position are computed once per block, into shared memory.
-template <int D, int UNROLL>
-__global__ void __launch_bounds__(256) head_rows_kernel(const HeadRowsParams p) {
+// D / 8 lanes hold one head row, 8 elements each as two groups of four, placed so
+// that both members of a rotated pair are in one lane (nothing is exchanged for the
+// rotation): in the half layout lane l holds [4l, 4l + 4) of the rotated part's
+// first half and the same of its second half, and the lanes behind share the rest
+// of the row; interleaved, 8 neighbours.  Either way a lane's pairs are 4l .. 4l + 3.
+//
+// A block takes `tokens` neighbouring tokens: their cosines and sines once, into
+// shared memory, then set after set of rows (one row per lane group), each for all
+// the tokens, four tokens' loads on their way together.  A lane group stays with
+// its head for a set, so weights and pointers are loop constants.  Between HBM and
+// the issue rate: 8192 tokens of 32 + 8 heads of 128 take 39 us (4.3 TB/s); with a
+// token's rows side by side and the halves exchanged by shuffles, at 1.4 times the
+// instructions, 53 us.
+constexpr int kHeadRowsMaxTokens = 16, kHeadRowsAhead = 4, kHeadRowsBps = 4;
+enum : int { kRowsDense = 0, kRowsBf16Cache = 1, kRowsE4m3Cache = 2 };
+
+template <int D, bool INTERLEAVED, int MODE>
+__global__ void __launch_bounds__(256, kHeadRowsBps) head_rows_kernel(const HeadRowsParams p, int tokens) {
   constexpr int G = D / 8;           // lanes per row
-  constexpr int NG = 256 / G;        // rows in flight per block and round
-  __shared__ float s_cos[D / 2], s_sin[D / 2];
-  const long long t = blockIdx.x;
+  constexpr int NG = 256 / G;        // rows of a set
+  constexpr int U = kHeadRowsAhead;
+  __shared__ __align__(16) float s_cos[kHeadRowsMaxTokens][D / 2], s_sin[kHeadRowsMaxTokens][D / 2];
   const int gid = threadIdx.x / G, l = threadIdx.x % G;
-  const int rows = p.Hq + p.Hkv + (p.has_v ? p.Hkv : 0);
-  const int r0 = blockIdx.y * (NG * UNROLL) + gid;
-  uint4 raw[UNROLL];
-#pragma unroll
-  for (int u = 0; u < UNROLL; ++u) {
-    const int r = r0 + u * NG;
-    raw[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < rows) {
-      const __nv_bfloat16* src = r < p.Hq ? p.q + t * p.q_stride + (long long)r * D
-                                 : r < p.Hq + p.Hkv ? p.k + t * p.k_stride + (long long)(r - p.Hq) * D
-                                                    : p.v + t * p.v_stride + (long long)(r - p.Hq - p.Hkv) * D;
-      raw[u] = *reinterpret_cast<const uint4*>(src + 8 * l);
-    }
-  }
-  long long slot = -1;
-  if (p.to_cache) {
-    slot = __ldg(p.slots + t);
-    if (slot >= p.n_slots) {
-      slot = -1;
-      if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.err, kErrIndex);
-    }
-  }
+  const long long t0 = (long long)blockIdx.x * tokens;
+  const int nt = p.T - t0 < tokens ? (int)(p.T - t0) : tokens;
+  const int rows = p.Hq + p.Hkv + (MODE != kRowsDense ? p.Hkv : 0);
   const int half = p.rot / 2;
+  // this lane's two groups of a row, in elements
+  const bool rotated = 4 * l < half;
+  const int ea = INTERLEAVED || half == 0 ? 8 * l : (rotated ? 4 * l : p.rot + 8 * (l - half / 4));
+  const int eb = !INTERLEAVED && rotated ? half + 4 * l : ea + 4;
   if (half > 0) {
-    if ((int)threadIdx.x < half) {
-      const double turns = (double)__ldg(p.positions + t) * __ldg(p.freqs + threadIdx.x) * 0.15915494309189533577;
+    for (int i = threadIdx.x; i < nt * half; i += 256) {
+      const int t = i / half, j = i - t * half;
+      const double turns = (double)__ldg(p.positions + t0 + t) * (__ldg(p.freqs + j) * 0.15915494309189533577);
       float s, c;
       sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
-      s_cos[threadIdx.x] = c * p.amplitude;
-      s_sin[threadIdx.x] = s * p.amplitude;
+      s_cos[t][j] = c * p.amplitude;
+      s_sin[t][j] = s * p.amplitude;
     }
     __syncthreads();
   }
-#pragma unroll
-  for (int u = 0; u < UNROLL; ++u) {
-    const int r = r0 + u * NG;
-    const bool live = r < rows;
-    const bool is_q = r < p.Hq, is_v = r >= p.Hq + p.Hkv;
-    float x[8];
-    unpack8(raw[u], x);
-    const __nv_bfloat16* w = is_v ? nullptr : (is_q ? p.q_weight : p.k_weight);
-    // (the shuffles below run on every lane: all 32 lanes of a warp stay together)
-    if (p.q_weight != nullptr || p.k_weight != nullptr) {
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-      for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (w != nullptr) {
-        const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-        float wf[8];
-        unpack8(*reinterpret_cast<const uint4*>(w + 8 * l), wf);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= inv * wf[i];
-      }
+  for (int r = blockIdx.y * NG + gid; r - gid < rows; r += gridDim.y * NG) {
+    if (r - (int)(threadIdx.x & 31) / G >= rows) break;  // none of the warp's rows is there
+    const bool live = r < rows, is_q = r < p.Hq, is_v = MODE != kRowsDense && r >= p.Hq + p.Hkv;
+    const int h = is_q ? r : (is_v ? r - p.Hq - p.Hkv : r - p.Hq);
+    const long long in_step = is_q ? p.q_stride : (is_v ? p.v_stride : p.k_stride);
+    const __nv_bfloat16* in = (is_q ? p.q : (is_v ? p.v : p.k)) + t0 * in_step + (long long)h * D;
+    // where dense rows go; the cache's rows follow the tokens' slots
+    const bool dense = MODE == kRowsDense || is_q;
+    const long long out_step = is_q ? p.q_out_stride : p.k_out_stride;
+    __nv_bfloat16* out = dense && live ? (is_q ? p.q_out : p.k_out) + t0 * out_step + (long long)h * D : nullptr;
+    const __nv_bfloat16* w = is_v || !live ? nullptr : (is_q ? p.q_weight : p.k_weight);
+    float wf[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    if (w != nullptr) {
+      const uint2 wa = __ldg(reinterpret_cast<const uint2*>(w + ea)), wb = __ldg(reinterpret_cast<const uint2*>(w + eb));
+      unpack8(make_uint4(wa.x, wa.y, wb.x, wb.y), wf);
     }
-    if (half > 0) {
-      if (p.interleaved) {
-        if (!is_v && 8 * l < p.rot) {
+    const bool turn = rotated && !is_v;
+    for (int i0 = 0; i0 < nt; i0 += U) {
+      uint2 ra[U], rb[U];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float c = s_cos[4 * l + i], s = s_sin[4 * l + i];
-            const float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = a * c - b * s;
-            x[2 * i + 1] = b * c + a * s;
+      for (int u = 0; u < U; ++u) {
+        ra[u] = rb[u] = make_uint2(0u, 0u);
+        if (live && i0 + u < nt) {
+          ra[u] = *reinterpret_cast<const uint2*>(in + ea);
+          rb[u] = *reinterpret_cast<const uint2*>(in + eb);
+        }
+        in += in_step;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u;
+        if (i >= nt) break;  // (the whole block)
+        float x[8];
+        unpack8(make_uint4(ra[u].x, ra[u].y, rb[u].x, rb[u].y), x);
+        // (the shuffles below run on every lane: all 32 lanes of a warp stay together)
+        if (p.q_weight != nullptr || p.k_weight != nullptr) {
+          float ss = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+          for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          const float inv = w != nullptr ? rsqrtf(ss * (1.f / D) + p.eps) : 1.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] *= wf[e] * inv;
+        }
+        if (turn) {
+          const float4 c4 = *reinterpret_cast<const float4*>(&s_cos[i][4 * l]);
+          const float4 s4 = *reinterpret_cast<const float4*>(&s_sin[i][4 * l]);
+          const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            constexpr int A = INTERLEAVED ? 2 : 1, B = INTERLEAVED ? 1 : 4;  // pair e: elements A e and A e + B
+            const float a0 = x[A * e], b0 = x[A * e + B];
+            x[A * e] = a0 * c[e] - b0 * s[e];
+            x[A * e + B] = b0 * c[e] + a0 * s[e];
           }
         }
-      } else {
-        const int hl = half / 8;  // lanes of one half
-        const int partner = l < hl ? l + hl : (l < 2 * hl ? l - hl : l);
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], partner, G);
-        if (!is_v && l < 2 * hl) {
-          const int c0 = 8 * (l < hl ? l : l - hl);
-          const float sign = l < hl ? -1.f : 1.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = x[i] * s_cos[c0 + i] + sign * (y[i] * s_sin[c0 + i]);
+        if (dense) {
+          if (live) {
+            const uint4 y = pack8(x);
+            *reinterpret_cast<uint2*>(out + ea) = make_uint2(y.x, y.y);
+            *reinterpret_cast<uint2*>(out + eb) = make_uint2(y.z, y.w);
+          }
+          out += out_step;
         }
-      }
-    }
-    if (!p.to_cache || is_q) {
-      if (live) {
-        __nv_bfloat16* dst = is_q ? p.q_out + t * p.q_out_stride + (long long)r * D
-                                  : p.k_out + t * p.k_out_stride + (long long)(r - p.Hq) * D;
-        *reinterpret_cast<uint4*>(dst + 8 * l) = pack8(x);
-      }
-    }
-    if (p.to_cache) {
-      const int h = is_v ? r - p.Hq - p.Hkv : r - p.Hq;
-      const bool store = live && !is_q && slot >= 0;
-      const long long row = slot * p.Hkv + h;
-      if (p.k_exp == nullptr) {
-        if (store)
-          reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(is_v ? p.v_pages : p.k_pages) + row * D)[l] = pack8(x);
-      } else {
-        uint32_t a = 0u;  // the largest magnitude, by its bits
+        if constexpr (MODE != kRowsDense) {
+          long long slot = __ldg(p.slots + t0 + i);
+          if (slot >= p.n_slots) {
+            if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.err, kErrIndex);
+            slot = -1;
+          }
+          const bool store = live && !is_q && slot >= 0;
+          const long long row = slot * p.Hkv + h;
+          if constexpr (MODE == kRowsBf16Cache) {
+            if (store) {
+              __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? p.v_pages : p.k_pages) + row * D;
+              const uint4 y = pack8(x);
+              *reinterpret_cast<uint2*>(dst + ea) = make_uint2(y.x, y.y);
+              *reinterpret_cast<uint2*>(dst + eb) = make_uint2(y.z, y.w);
+            }
+          } else {
+            uint32_t a = 0u;  // the largest magnitude, by its bits
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;
-          a = a > b ? a : b;
-        }
+            for (int e = 0; e < 8; ++e) a = max(a, __float_as_uint(x[e]) & 0x7FFFFFFFu);
 #pragma unroll
-        for (int o = G / 2; o > 0; o >>= 1) {
-          const uint32_t b = __shfl_xor_sync(0xffffffffu, a, o);
-          a = a > b ? a : b;
-        }
-        const uint32_t e = e4m3_row_exponent(a);
-        const float m = __uint_as_float((e == kExpNaN ? 127u : 254u - e) << 23);  // 2^-(e - 127)
-        if (store) {
-          const uint2 codes = make_uint2(ptx::pack_e4m3x4(x[0] * m, x[1] * m, x[2] * m, x[3] * m),
-                                         ptx::pack_e4m3x4(x[4] * m, x[5] * m, x[6] * m, x[7] * m));
-          reinterpret_cast<uint2*>(reinterpret_cast<unsigned char*>(is_v ? p.v_pages : p.k_pages) + row * D)[l] = codes;
-          if (l == 0) (is_v ? p.v_exp : p.k_exp)[row] = (unsigned char)e;
+            for (int o = G / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+            const uint32_t e = e4m3_row_exponent(a);
+            const float m = __uint_as_float((e == kExpNaN ? 127u : 254u - e) << 23);  // 2^-(e - 127)
+            if (store) {
+              unsigned char* dst = static_cast<unsigned char*>(is_v ? p.v_pages : p.k_pages) + row * D;
+              *reinterpret_cast<uint32_t*>(dst + ea) = ptx::pack_e4m3x4(x[0] * m, x[1] * m, x[2] * m, x[3] * m);
+              *reinterpret_cast<uint32_t*>(dst + eb) = ptx::pack_e4m3x4(x[4] * m, x[5] * m, x[6] * m, x[7] * m);
+              if (l == 0) (is_v ? p.v_exp : p.k_exp)[row] = (unsigned char)e;
+            }
+          }
         }
       }
     }
@@ -214,10 +225,12 @@ struct KvReadParams {
 };
 
 // One warp per token: its sequence by bisection over the boundaries, its page
-// from the table, then Hkv * d contiguous values of K and of V (16 bytes of
-// output per lane and step).
+// from the table, then the token's Hkv * d contiguous values of K and of V, 16
+// bytes read per lane and step.  Bound by HBM (4 tokens a warp, with fewer warps to
+// hide the two look-ups: 127 us instead of 100 on 62000 tokens of 8 x 128 e4m3).
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(256) kv_read_kernel(const KvReadParams p) {
+  constexpr int PE = E4M3 ? 16 : 8;  // elements of a piece
   const long long t = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (t >= p.T) return;
@@ -226,40 +239,41 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const KvReadParams p) {
     const int mid = (lo + hi + 1) / 2;
     if ((long long)__ldg(p.cu + mid) <= t) lo = mid; else hi = mid - 1;
   }
-  if (lo >= p.n_seqs) return;  // behind the last sequence
   const int start = __ldg(p.cu + lo);
-  if (start > t) return;       // in front of the first
-  const long long pos = t - start;
-  const long long pi = pos >> p.page_shift;
+  if (lo >= p.n_seqs || start > t) return;  // behind the last sequence, or in front of the first
+  const long long pos = t - start, pi = pos >> p.page_shift;
   int page = -1;
   if (start >= 0 && pi < p.table_width) page = __ldg(p.table + (long long)lo * p.table_width + pi);
   const bool ok = page >= 0 && page < p.n_pages;
   if (!ok && lane == 0) atomicOr(p.err, kErrIndex);
   const long long row = ok ? (((long long)page << p.page_shift) + (pos & ((1 << p.page_shift) - 1))) * p.Hkv : 0;
-  const int n = p.Hkv * (D / 8);  // 8-element pieces of a token
+  const int n = p.Hkv * (D / PE);
+  uint4* ko = reinterpret_cast<uint4*>(p.k + t * p.Hkv * D);
+  uint4* vo = reinterpret_cast<uint4*>(p.v + t * p.Hkv * D);
+  const uint4* ki = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k_pages) + row * D * (E4M3 ? 1 : 2));
+  const uint4* vi = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.v_pages) + row * D * (E4M3 ? 1 : 2));
+#pragma unroll 2
   for (int c = lane; c < n; c += 32) {
-    uint4 w[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const void* src = x == 0 ? p.k_pages : p.v_pages;
-      w[x] = make_uint4(0u, 0u, 0u, 0u);
-      if (!ok) continue;
+      uint4* out = x == 0 ? ko : vo;
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (ok) w = __ldg((x == 0 ? ki : vi) + c);
       if constexpr (!E4M3) {
-        w[x] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(src) + row * D) + c);
+        out[c] = w;
       } else {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const unsigned char*>(src) + row * D) + c);
-        const uint32_t e = __ldg((x == 0 ? p.k_exp : p.v_exp) + row + c / (D / 8));
-        const E4m3Factor f = e4m3_factor(e);
-        const uint32_t h[4] = {__byte_perm(q.x, 0u, 0x1404), __byte_perm(q.x, 0u, 0x3424), __byte_perm(q.y, 0u, 0x1404),
-                               __byte_perm(q.y, 0u, 0x3424)};
-        uint32_t o[4];
+        const E4m3Factor f = e4m3_factor(ok ? __ldg((x == 0 ? p.k_exp : p.v_exp) + row + c / (D / PE)) : 127u);
+        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+        uint32_t o[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = bf16x2_mul(bf16x2_mul(e4m3_hi_bits(h[i]), f.m), f.more);
-        w[x] = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int y = 0; y < 4; ++y) {
+          o[2 * y] = bf16x2_mul(bf16x2_mul(e4m3_hi_bits(__byte_perm(in[y], 0u, 0x1404)), f.m), f.more);
+          o[2 * y + 1] = bf16x2_mul(bf16x2_mul(e4m3_hi_bits(__byte_perm(in[y], 0u, 0x3424)), f.m), f.more);
+        }
+        out[2 * c] = make_uint4(o[0], o[1], o[2], o[3]);
+        out[2 * c + 1] = make_uint4(o[4], o[5], o[6], o[7]);
       }
     }
-    reinterpret_cast<uint4*>(p.k + t * p.Hkv * D)[c] = w[0];
-    reinterpret_cast<uint4*>(p.v + t * p.Hkv * D)[c] = w[1];
   }
 }
 

@@ -396,6 +396,12 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// The larger of the two, NaN if either is.
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __host__ __device__ constexpr uint64_t f2_const(uint32_t bits) { return ((uint64_t)bits << 32) | bits; }
 
 __device__ __forceinline__ float ex2(float x) {

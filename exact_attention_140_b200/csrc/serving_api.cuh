@@ -56,29 +56,44 @@ void fill_rope(HeadRowsParams* p, const attn_rope_t* r, const long long* positio
   p->positions = positions;
 }
 
-template <int D>
-int launch_head_rows_d(const HeadRowsParams& p, long long T, DeviceState* st, cudaStream_t s) {
+// Tokens of a block: several in a long call (their weights, pointers and cosines
+// are shared), one in a short one, whose rows are spread over blocks instead.
+template <int D, bool INTERLEAVED>
+int launch_head_rows_d(const HeadRowsParams& p, int mode, DeviceState* st, cudaStream_t s) {
   constexpr int NG = 256 / (D / 8);
-  const int rows = p.Hq + p.Hkv + (p.has_v ? p.Hkv : 0);
-  // four rows per lane group hide the loads' latency in a long grid; a short
-  // one spreads a token's rows over more blocks instead
-  const bool wide = T * ((rows + NG * 4 - 1) / (NG * 4)) >= 4ll * st->num_sms;
-  const unsigned gy = (unsigned)(wide ? (rows + NG * 4 - 1) / (NG * 4) : (rows + NG - 1) / NG);
-  if (gy > 65535u) return ATTN_ERR_UNSUPPORTED;
-  ATTN_LOGF("attn: head_rows_kernel<%d, %d> grid=(%lld,%u) block=256 Hq=%d Hkv=%d rot=%d cache=%s\n", D, wide ? 4 : 1, T,
-            gy, p.Hq, p.Hkv, p.rot, !p.to_cache ? "no" : (p.k_exp != nullptr ? "e4m3" : "bf16"));
-  if (wide)
-    head_rows_kernel<D, 4><<<dim3((unsigned)T, gy), 256, 0, s>>>(p);
-  else
-    head_rows_kernel<D, 1><<<dim3((unsigned)T, gy), 256, 0, s>>>(p);
+  const int rows = p.Hq + p.Hkv + (mode != kRowsDense ? p.Hkv : 0), sets = (rows + NG - 1) / NG;
+  const long long fill = (long long)kHeadRowsBps * st->num_sms;  // blocks the GPU holds at once
+  // the count whose blocks come out nearest to whole rounds of the GPU
+  long long tokens = 1;
+  double best = 0.0;
+  for (long long n = kHeadRowsMaxTokens; n >= 1; --n) {
+    const long long b = (p.T + n - 1) / n;
+    const double even = (double)p.T / (double)(n * ((b + fill - 1) / fill) * fill);
+    if (even > best + 0.02) {
+      best = even;
+      tokens = n;
+    }
+  }
+  const long long gx = (p.T + tokens - 1) / tokens;
+  long long gy = fill / gx;
+  gy = gy < 1 ? 1 : (gy > sets ? sets : gy);
+  const dim3 grid((unsigned)gx, (unsigned)gy);
+  ATTN_LOGF("attn: head_rows_kernel<%d, %s, %d> grid=(%u,%u) block=256 T=%lld tokens=%lld Hq=%d Hkv=%d rot=%d\n", D,
+            INTERLEAVED ? "interleaved" : "half", mode, grid.x, grid.y, p.T, tokens, p.Hq, p.Hkv, p.rot);
+  switch (mode) {
+    case kRowsDense: head_rows_kernel<D, INTERLEAVED, kRowsDense><<<grid, 256, 0, s>>>(p, (int)tokens); break;
+    case kRowsBf16Cache: head_rows_kernel<D, INTERLEAVED, kRowsBf16Cache><<<grid, 256, 0, s>>>(p, (int)tokens); break;
+    default: head_rows_kernel<D, INTERLEAVED, kRowsE4m3Cache><<<grid, 256, 0, s>>>(p, (int)tokens); break;
+  }
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
-int launch_head_rows(const HeadRowsParams& p, int d, long long T, DeviceState* st, cudaStream_t s) {
+int launch_head_rows(HeadRowsParams& p, int d, long long T, int mode, DeviceState* st, cudaStream_t s) {
   if (p.Hq + p.Hkv == 0) return ATTN_OK;
+  p.T = T;
   switch (d) {
-    case 64: return launch_head_rows_d<64>(p, T, st, s);
-    case 128: return launch_head_rows_d<128>(p, T, st, s);
-    default: return launch_head_rows_d<256>(p, T, st, s);
+    case 64: return p.interleaved ? launch_head_rows_d<64, true>(p, mode, st, s) : launch_head_rows_d<64, false>(p, mode, st, s);
+    case 128: return p.interleaved ? launch_head_rows_d<128, true>(p, mode, st, s) : launch_head_rows_d<128, false>(p, mode, st, s);
+    default: return p.interleaved ? launch_head_rows_d<256, true>(p, mode, st, s) : launch_head_rows_d<256, false>(p, mode, st, s);
   }
 }
 
@@ -140,12 +155,21 @@ PagedPlan paged_plan(const attn_kv_cache_t* c, int Tq, int n_seqs, int max_q, in
   if (rows > 64 && c->n_pages > 0) {
     pl.items = ragged_max_items(Tq, n_seqs, Hq, Hkv, c->d);
     const int g = ragged_rows_per_token(Hq, Hkv);
-    // about two blocks per SM, windows of 512 keys at least
+    // Windows by an estimate in key times (one block, 256 rows, about 16 ns a key):
+    // the waves of blocks times a window's keys and a block's fixed cost, and
+    // writing and merging the partial rows (about 4 TB/s, 5 us to begin with).
     const long long blocks = ((long long)Tq * g / ragged_block_rows(c->d) + (n_seqs + 1) / 2) * (g > 1 ? Hkv : Hq);
-    long long want = (2ll * kSms + blocks - 1) / (blocks > 0 ? blocks : 1);
-    const long long cap = max_kv / 512;
-    want = want > cap ? cap : want;
-    want = want < 1 ? 1 : want;
+    long long want = 1;
+    double best = 0.0;
+    for (long long n = 1; n <= 16 && (n == 1 || max_kv / n >= 512); ++n) {
+      const double waves = (double)((blocks * n + kSms - 1) / kSms);
+      const double merge = n == 1 ? 0.0 : 300.0 + 2.0 * n * Tq * Hq * c->d * 4 / 64000.0;
+      const double t = waves * ((double)max_kv / n + 600.0) + merge;
+      if (n == 1 || t < best) {
+        best = t;
+        want = n;
+      }
+    }
     const long long w = (((long long)max_kv + want - 1) / want + 127) / 128 * 128;
     pl.window = (int)(w < 128 ? 128 : w);
     pl.n_windows = max_kv > pl.window ? (int)(((long long)max_kv + pl.window - 1) / pl.window) : 1;
@@ -243,14 +267,15 @@ int launch_paged(const PagedParams& p, const PagedPlan& pl, const attn_kv_cache_
 
 // ---------------------------------------------------------------- packed sequences on tcgen05
 // The long-range configurations over packed sequences (1) or a paged cache (2
-// bf16, 3 e4m3), all exponentials on the hardware unit: the software share
-// would lose a NaN score, and over packed sequences it gains nothing (1715
-// against 1728 us at 8192 tokens causal, 331 against 320 us on 512-token chunks);
-// the heads of a group are always stacked where the group divides the tile: a
+// bf16, 3 e4m3).  Exponentials in software at d = 128 as there (4 x 4096 tokens
+// causal: 568 us without, 555 with), except over an e4m3 cache, whose expanding
+// warps need the issue slots, and at d = 64, where it gains nothing (the batch of
+// prompts up to 1024: 32.0 us without, 32.8 with).
+// The heads of a group are always stacked where the group divides the tile: a
 // block then covers fewer tokens, which wastes less of a causal block's diagonal
 // and of a short sequence, and a key tile is read once per group.
 template <bool C, int R> using CfgRagD64 = FwdCfg<64, 128, 2, 3, 3, C, false, 0, 1, false, 1, true, false, R>;
-template <bool C, int R> using CfgRagD128 = FwdCfg<128, 128, 2, 2, 2, C, false, 0, 1, false, 1, true, false, R>;
+template <bool C, int R> using CfgRagD128 = FwdCfg<128, 128, 2, 2, 2, C, false, R == 3 ? 0 : (C ? 2 : 1), 1, false, 1, true, false, R>;
 template <bool C, int R> using CfgRagD256 = FwdCfg<256, 64, 1, 2, 2, C, false, 0, 2, false, 1, true, false, R>;
 
 int ragged_block_rows(int d) { return d == 256 ? 128 : 256; }
@@ -463,7 +488,7 @@ int attn_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, lo
   p.Hkv = Hkv;
   fill_rope(&p, rope, positions);
   p.err = st->err;
-  return launch_head_rows(p, d, T, st, static_cast<cudaStream_t>(stream));
+  return launch_head_rows(p, d, T, kRowsDense, st, static_cast<cudaStream_t>(stream));
 }
 
 int attn_kv_write(const attn_kv_cache_t* cache, const void* k, const void* v, long long T, long long k_stride,
@@ -496,8 +521,6 @@ int attn_kv_write(const attn_kv_cache_t* cache, const void* k, const void* v, lo
   p.q_out_stride = q_out_stride;
   p.Hq = Hq;
   p.Hkv = Hkv;
-  p.has_v = true;
-  p.to_cache = true;
   p.slots = slots;
   p.n_slots = (long long)cache->n_pages * cache->page_size;
   p.k_pages = cache->k_pages;
@@ -506,7 +529,8 @@ int attn_kv_write(const attn_kv_cache_t* cache, const void* k, const void* v, lo
   p.v_exp = cache->v_exp;
   if (rope != nullptr) fill_rope(&p, rope, positions);
   p.err = st->err;
-  return launch_head_rows(p, d, T, st, static_cast<cudaStream_t>(stream));
+  return launch_head_rows(p, d, T, cache->dtype == ATTN_FP8_E4M3 ? kRowsE4m3Cache : kRowsBf16Cache, st,
+                          static_cast<cudaStream_t>(stream));
 }
 
 int attn_kv_read(const attn_kv_cache_t* cache, const int* table, int table_width, const int* cu, int n_seqs, void* k,
