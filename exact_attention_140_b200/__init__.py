@@ -622,7 +622,7 @@ def _outputs(q, o, lse, return_lse):
         _need(lse.shape == (H, T) and lse.dtype is torch.float32 and lse.is_contiguous(),
               "lse must be contiguous fp32 [Hq, T]")
     elif return_lse:
-        lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((H, T), dtype=torch.float32)
         new.append(lse)
     return o, lse, new
 
@@ -644,7 +644,7 @@ def attention_varlen(q, k, v, cu_q, cu_k, causal: bool = False, scale: float | N
     nbytes = _lib.attn_fwd_varlen_workspace_bytes(Tq, n, Hq, Hkv, d)
     ws = None
     if nbytes > 0:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        ws = q.new_empty(nbytes // 2 + 1)  # (bf16 elements)
         new.append(ws)
     rc = _lib.attn_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(lse), Tq, Tk, n,
                               cu_q.data_ptr(), cu_k.data_ptr(), Hq, Hkv, d, qs, ks, vs, int(causal),
@@ -680,7 +680,7 @@ def attention_paged(q, cache, table, kv_lens, cu_q=None, max_q=None, max_kv=None
     nbytes = _lib.attn_fwd_paged_workspace_bytes(cache.struct, Tq, n, max_q, Hq, max_kv)
     ws = None
     if nbytes > 0:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        ws = q.new_empty(nbytes // 2 + 1)  # (bf16 elements)
         new.append(ws)
     rc = _lib.attn_fwd_paged(q.data_ptr(), cache.struct, o.data_ptr(), _ptr(lse), Tq, n, max_q, _ptr(cu_q),
                              table.data_ptr(), width, kv_lens.data_ptr(), max_kv, Hq, qs, int(causal),

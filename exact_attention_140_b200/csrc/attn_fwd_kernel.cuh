@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
             float x0, x1;
             ptx::unf2(x, x0, x1);
             if (((16 * ch + c) % 8) < Cfg::EMU) {
-              exp2_soft2<Cfg::RAGGED != 0>(x0, x1, e0, e1);
+              exp2_soft2(x0, x1, e0, e1);
             } else {
               e0 = ptx::ex2(x0);
               e1 = ptx::ex2(x1);
@@ -376,9 +376,7 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
       if constexpr (Cfg::FP8) inv *= __ldg(p.dv);
       float lse = l > 0.f ? (m_ref + log2f(l)) * 0.6931471805599453f : -INFINITY;
       if constexpr (Cfg::RAGGED != 0) {
-        // a row whose scores hold a NaN (1e30: from the software exponential; a
-        // sum of weights is under 2^8 times the keys)
-        if (!(l < 1e30f)) inv = lse = __uint_as_float(0x7FFFFFFFu);
+        if (l != l) inv = lse = l;  // a row whose scores hold a NaN
       }
       // first element of the row in [tokens, Hq, D], and its place in lse
       long long tok, lse_at;

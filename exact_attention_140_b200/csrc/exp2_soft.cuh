@@ -23,13 +23,9 @@ namespace attn {
 constexpr uint32_t kExpMagicBits = 0x4B400000u;  // 1.5 * 2^23
 constexpr float kExpC1 = 0.693282723f, kExpC2 = 0.242211044f, kExpC3 = 0.0550097041f;
 
-// KEEP_NAN: a NaN is not clamped away but comes out as 3.4e38 (its bits run
-// through the integer step), far above any sum of exponentials of a softmax row,
-// by which the caller can tell.
-template <bool KEEP_NAN = false>
 __device__ __forceinline__ void exp2_soft2(float x0, float x1, float& y0, float& y1) {
   using namespace ptx;
-  const uint64_t x = KEEP_NAN ? f2(fmax_nan(x0, -125.f), fmax_nan(x1, -125.f)) : f2(fmaxf(x0, -125.f), fmaxf(x1, -125.f));
+  const uint64_t x = f2(fmaxf(x0, -125.f), fmaxf(x1, -125.f));
   const uint64_t t = fadd2(x, f2_const(kExpMagicBits));
   const uint64_t jf = fsub2(t, f2_const(kExpMagicBits));
   const uint64_t f = fsub2(x, jf);

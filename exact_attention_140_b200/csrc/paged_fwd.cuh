@@ -63,6 +63,7 @@ struct PagedParams : PagedSeqs {
   const unsigned char *k_exp, *v_exp;
   int n_pages, page_shift;
   int causal;
+  int row_tiles;             // CLUSTER: of a sequence of max_q tokens
   float sl2;                 // scale * log2(e)
   // workspace: units in front of each sequence and the units of a block, then the
   // partial rows [2 * blocks][block rows][D] and their LSE [2 * blocks][block rows]
@@ -169,7 +170,12 @@ __device__ __forceinline__ PagedShape paged_shape(const SeqRange& r, int group, 
   return x;
 }
 
-template <class Cfg>
+// CLUSTER: a segment belongs to a cluster of kPagedCluster blocks, which cut its
+// units into equal runs and merge their rows through one another's shared memory.
+// For calls that small that the second launch of the merge would take as long as
+// the attention.
+constexpr int kPagedCluster = 8;
+template <class Cfg, bool CLUSTER>
 __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
     paged_fwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const PagedParams p) {
@@ -188,30 +194,9 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(psm + Cfg::OFF_ABORT);
   const WaitCtx wc{abort_flag, p.err, p.timeout_ns};
 
-  ptx::grid_dep_launch();
+  if constexpr (!CLUSTER) ptx::grid_dep_launch();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = p.group;
-
-  // ---- this block's run of units: a scan over the sequences, each thread
-  // taking a contiguous share of them
-  long long* s_scan = reinterpret_cast<long long*>(psm + Cfg::OFF_SCAN);
-  const int per = (p.n_seqs + Cfg::NTHREADS - 1) / Cfg::NTHREADS;
-  const int sq0 = tid * per, sq1 = sq0 + per < p.n_seqs ? sq0 + per : p.n_seqs;
-  auto units_of = [&](int s) -> long long {
-    const SeqRange r = paged_seq(p, s);
-    if (r.bad) atomicOr(p.err, kErrIndex);
-    const PagedShape x = paged_shape(r, g, Cfg::ROWS, TK);
-    return (long long)x.row_tiles * p.Hkv * x.units;
-  };
-  long long mine = 0;
-  for (int s = sq0; s < sq1; ++s) mine += units_of(s);
-  long long upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += y;
-  }
-  if (lane == 31) s_scan[warp] = upto;
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
       ptx::mbar_init(full(i), E4M3 ? 33 : 1);
@@ -220,37 +205,73 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
     *abort_flag = 0u;
     ptx::fence_mbar_init();
   }
-  __syncthreads();
-  long long total = 0, front = upto - mine;
+
+  // ---- this block's run of units [u_begin, u_end): of all units, or (CLUSTER) of
+  // its segment's
+  long long* s_scan = reinterpret_cast<long long*>(psm + Cfg::OFF_SCAN);
+  long long u_begin, u_end;
+  if constexpr (CLUSTER) {
+    const int seg = (int)blockIdx.x / kPagedCluster, per_seq = p.row_tiles * p.Hkv;
+    const SeqRange r = paged_seq(p, seg / per_seq);
+    if (r.bad && tid == 0) atomicOr(p.err, kErrIndex);
+    const PagedShape x = paged_shape(r, g, Cfg::ROWS, TK);
+    if (seg % per_seq / p.Hkv >= x.row_tiles) return;  // (the whole cluster)
+    const int share = (x.units + kPagedCluster - 1) / kPagedCluster;
+    u_begin = (long long)share * ptx::cluster_rank();
+    u_end = u_begin + share < x.units ? u_begin + share : x.units;
+    __syncthreads();
+  } else {
+    // a scan over the sequences, each thread taking a contiguous share of them
+    const int per = (p.n_seqs + Cfg::NTHREADS - 1) / Cfg::NTHREADS;
+    const int sq0 = tid * per, sq1 = sq0 + per < p.n_seqs ? sq0 + per : p.n_seqs;
+    auto units_of = [&](int s) -> long long {
+      const SeqRange r = paged_seq(p, s);
+      if (r.bad) atomicOr(p.err, kErrIndex);
+      const PagedShape x = paged_shape(r, g, Cfg::ROWS, TK);
+      return (long long)x.row_tiles * p.Hkv * x.units;
+    };
+    long long mine = 0;
+    for (int s = sq0; s < sq1; ++s) mine += units_of(s);
+    long long upto = mine;
 #pragma unroll
-  for (int i = 0; i < Cfg::NTHREADS / 32; ++i) {
-    if (i < warp) front += s_scan[i];
-    total += s_scan[i];
-  }
-  const long long share = (total + gridDim.x - 1) / gridDim.x;
-  const long long u_begin = share * blockIdx.x, u_end = u_begin + share < total ? u_begin + share : total;
-  if (blockIdx.x == 0) {  // for the merge
-    long long at = front;
-    for (int s = sq0; s < sq1; ++s) {
-      p.base[s] = at;
-      at += units_of(s);
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
     }
-    if (tid == 0) p.base[p.n_seqs] = share;
-  }
-  if (u_begin >= u_end) return;
-  __syncthreads();  // (the warp sums have been read)
-  if (front <= u_begin && u_begin < front + mine) {
-    long long at = front;
-    int s = sq0;
-    for (;; ++s) {
-      const long long n = units_of(s);
-      if (u_begin < at + n) break;
-      at += n;
+    if (lane == 31) s_scan[warp] = upto;
+    __syncthreads();
+    long long total = 0, front = upto - mine;
+#pragma unroll
+    for (int i = 0; i < Cfg::NTHREADS / 32; ++i) {
+      if (i < warp) front += s_scan[i];
+      total += s_scan[i];
     }
-    s_scan[0] = s;
-    s_scan[1] = at;
+    const long long share = (total + gridDim.x - 1) / gridDim.x;
+    u_begin = share * blockIdx.x;
+    u_end = u_begin + share < total ? u_begin + share : total;
+    if (blockIdx.x == 0) {  // for the merge
+      long long at = front;
+      for (int s = sq0; s < sq1; ++s) {
+        p.base[s] = at;
+        at += units_of(s);
+      }
+      if (tid == 0) p.base[p.n_seqs] = share;
+    }
+    if (u_begin >= u_end) return;
+    __syncthreads();  // (the warp sums have been read)
+    if (front <= u_begin && u_begin < front + mine) {
+      long long at = front;
+      int s = sq0;
+      for (;; ++s) {
+        const long long n = units_of(s);
+        if (u_begin < at + n) break;
+        at += n;
+      }
+      s_scan[0] = s;
+      s_scan[1] = at;
+    }
+    __syncthreads();
   }
-  __syncthreads();
 
   // ---- the run as portions: part (from unit `u` on) of a segment (sequence s,
   // row tile rt, head kh), in order; producer and consumers walk it alike
@@ -265,7 +286,7 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
     bool first, last;  // it holds the segment's first, last unit
   };
   auto settle = [&](Portion& x) {
-    const long long stop = x.at + x.sh.units < u_end ? x.at + x.sh.units : u_end;
+    const long long stop = x.at + x.sh.units < u_end ? x.at + x.sh.units : u_end;  // (CLUSTER: may be no more than x.u)
     x.first = x.u == x.at;
     x.last = x.at + x.sh.units <= u_end;
     x.k0 = (int)(x.u - x.at) * TK;
@@ -282,6 +303,18 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
   };
   auto first_portion = [&]() -> Portion {
     Portion x;
+    if constexpr (CLUSTER) {
+      const int seg = (int)blockIdx.x / kPagedCluster, in_seq = seg % (p.row_tiles * p.Hkv);
+      x.s = seg / (p.row_tiles * p.Hkv);
+      x.sr = paged_seq(p, x.s);
+      x.sh = paged_shape(x.sr, g, Cfg::ROWS, TK);
+      x.rt = in_seq / p.Hkv;
+      x.kh = in_seq % p.Hkv;
+      x.at = 0;
+      x.u = u_begin;
+      settle(x);
+      return x;
+    }
     x.s = (int)s_scan[0];
     x.sr = paged_seq(p, x.s);
     x.sh = paged_shape(x.sr, g, Cfg::ROWS, TK);
@@ -294,6 +327,7 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
     return x;
   };
   auto next_portion = [&](Portion& x) -> bool {  // false at the end of the run
+    if constexpr (CLUSTER) return false;
     x.at += x.sh.units;
     if (x.at >= u_end) return false;
     x.u = x.at;
@@ -410,6 +444,10 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
       if (f > 0) wait_bar_drain<kRoleProducer>(full(i), (uint32_t)((f - 1) & 1), wc, kSiteKFull);
     }
     __syncthreads();
+    if constexpr (CLUSTER) {
+      ptx::cluster_sync();
+      ptx::cluster_sync();
+    }
     return;
   }
 
@@ -835,7 +873,7 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
     }
     ptx::bar_sync(1, 128);
     constexpr int PPR = D / 8;  // 8-column pieces of a row
-    for (int i = tid; i < Cfg::ROWS * PPR; i += 128) {
+    for (int i = tid; !CLUSTER && i < Cfg::ROWS * PPR; i += 128) {
       const int r = i / PPR, pc = i % PPR;
       if (row0 + r >= rows) break;
       const float* row = so + r * Cfg::OSTR;
@@ -857,6 +895,40 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
     if (!ptx::bar_red_and(1, 128, ok)) break;  // (then the merge rows and references are free again)
   } while (next_portion(x));
   __syncthreads();
+  if constexpr (CLUSTER) {
+    // every block holds its rows and their LSE; block k merges rows k, k + 8, ...
+    ptx::cluster_sync();
+    const long long rows = (long long)x.sr.nq * g, row0 = (long long)x.rt * Cfg::ROWS;
+    for (int r = (int)ptx::cluster_rank(); r < Cfg::ROWS && row0 + r < rows; r += kPagedCluster) {
+      const uint32_t row = sb + Cfg::OFF_MRG + (uint32_t)(r * Cfg::OSTR) * 4u;
+      float wt[kPagedCluster], mx = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < kPagedCluster; ++k) {
+        wt[k] = ptx::ld_peer_f32(row + D * 4u, (uint32_t)k);
+        mx = fmaxf(mx, wt[k]);
+      }
+      const float mu = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+      for (int k = 0; k < kPagedCluster; ++k) {
+        wt[k] = expf(wt[k] - mu);
+        sum += wt[k];
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const long long pr = row0 + r;
+      const int t = x.sr.q0 + (int)(pr / g), h = x.kh * g + (int)(pr % g);
+      for (int col = tid; col < D; col += 128) {
+        float y = 0.f;
+#pragma unroll
+        for (int k = 0; k < kPagedCluster; ++k) {
+          const float v = ptx::ld_peer_f32(row + (uint32_t)col * 4u, (uint32_t)k);
+          y = wt[k] == 0.f ? y : fmaf(wt[k], v, y);
+        }
+        p.o[((long long)t * p.Hq + h) * D + col] = __float2bfloat16_rn(y * inv);
+      }
+      if (tid == 0 && p.lse != nullptr) p.lse[(long long)h * p.Tq + t] = sum == 0.f ? -INFINITY : mu + logf(sum);
+    }
+    ptx::cluster_sync();  // (a block's rows stay until all have read them)
+  }
 }
 
 // One output row from S partial rows, by a warp: part w is row slot(w) of o_part

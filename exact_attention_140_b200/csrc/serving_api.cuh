@@ -113,7 +113,8 @@ int launch_kv_read(const KvReadParams& p, cudaStream_t s) {
 // over listed items, each sequence's keys cut into n_windows windows where the
 // items are too few for the GPU.
 struct PagedPlan {
-  int size, block_rows, unit, blocks;
+  int size, block_rows, unit, row_tiles, blocks;
+  bool cluster;
   long long items;
   int window, n_windows;
 };
@@ -179,14 +180,20 @@ PagedPlan paged_plan(const attn_kv_cache_t* c, int Tq, int n_seqs, int max_q, in
   pl.block_rows = paged_block_rows(c->d, pl.size);
   const PagedGeometry ge = paged_geometry(c->d, c->dtype == ATTN_FP8_E4M3, pl.size);
   pl.unit = ge.unit;
-  const long long units = (long long)n_seqs * ((rows + pl.block_rows - 1) / pl.block_rows) * Hkv *
-                          (max_kv > pl.unit ? ((long long)max_kv + pl.unit - 1) / pl.unit : 1);
-  const long long most = (long long)kSms * ge.blocks_per_sm;
-  pl.blocks = (int)(units < most ? units : most);
+  pl.row_tiles = (int)((rows + pl.block_rows - 1) / pl.block_rows);
+  const long long units = max_kv > pl.unit ? ((long long)max_kv + pl.unit - 1) / pl.unit : 1;  // of a segment
+  const long long segments = (long long)n_seqs * pl.row_tiles * Hkv, most = (long long)kSms * ge.blocks_per_sm;
+  // a cluster per segment where the clusters fit the GPU at once and their blocks
+  // have no more than a few units each
+  pl.cluster = units > 1 && units <= 4 * kPagedCluster && segments * kPagedCluster <= most;
+  if (pl.cluster)
+    pl.blocks = (int)segments * kPagedCluster;
+  else
+    pl.blocks = (int)(segments * units < most ? segments * units : most);
   return pl;
 }
 // Workspace.  paged_fwd_kernel: a long long per sequence and one, the partial
-// rows, their LSE.  tcgen05: the item list, the windows' partial rows, their LSE.
+// rows, their LSE (nothing for clusters).  tcgen05: the item list, the windows' partial rows, their LSE.
 struct PagedSpace {
   long long head, o, lse;  // bytes of each
   long long all() const { return head + o + lse; }
@@ -202,6 +209,7 @@ PagedSpace paged_space(const PagedPlan& pl, long long Tq, long long n_seqs, long
     }
     return s;
   }
+  if (pl.cluster) return s;
   s.head = round((n_seqs + 1) * 8);
   s.o = 2ll * pl.blocks * pl.block_rows * d * 4;
   s.lse = round(2ll * pl.blocks * pl.block_rows * 4);
@@ -209,9 +217,10 @@ PagedSpace paged_space(const PagedPlan& pl, long long Tq, long long n_seqs, long
 }
 
 template <class Cfg>
-int launch_paged_cfg(const PagedParams& p, int blocks, const attn_kv_cache_t* c, DeviceState* st, cudaStream_t s) {
-  static std::atomic<unsigned> attr_set[kMaxDevices];
-  int rc = set_smem_once(paged_fwd_kernel<Cfg>, (int)Cfg::SMEM, attr_set, st);
+int launch_paged_cfg(const PagedParams& p, const PagedPlan& pl, const attn_kv_cache_t* c, DeviceState* st, cudaStream_t s) {
+  static std::atomic<unsigned> attr_set[kMaxDevices], attr_set_cluster[kMaxDevices];
+  int rc = pl.cluster ? set_smem_once(paged_fwd_kernel<Cfg, true>, (int)Cfg::SMEM, attr_set_cluster, st)
+                      : set_smem_once(paged_fwd_kernel<Cfg, false>, (int)Cfg::SMEM, attr_set, st);
   if (rc != ATTN_OK) return rc;
   CUtensorMap tk, tv;
   std::memset(&tk, 0, sizeof(tk));
@@ -223,19 +232,33 @@ int launch_paged_cfg(const PagedParams& p, int blocks, const attn_kv_cache_t* c,
         encode(&tv, c->v_pages, c->n_pages, c->page_size, c->Hkv, c->d, rows) != ATTN_OK)
       return ATTN_ERR_CUDA;
   }
-  ATTN_LOGF("attn: paged_fwd_kernel<%d, %s, NT=%d RW=%d> grid=(%d) block=%d smem=%u seqs=%d max_q=%d Hq=%d Hkv=%d\n",
-            Cfg::D, Cfg::E4M3 ? "e4m3" : "bf16", Cfg::NT, Cfg::RW, blocks, Cfg::NTHREADS, (unsigned)Cfg::SMEM, p.n_seqs,
-            p.max_q, p.Hq, p.Hkv);
-  paged_fwd_kernel<Cfg><<<(unsigned)blocks, Cfg::NTHREADS, Cfg::SMEM, s>>>(tk, tv, p);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  ATTN_LOGF("attn: paged_fwd_kernel<%d, %s, NT=%d RW=%d%s> grid=(%d) block=%d smem=%u seqs=%d max_q=%d Hq=%d Hkv=%d\n",
+            Cfg::D, Cfg::E4M3 ? "e4m3" : "bf16", Cfg::NT, Cfg::RW, pl.cluster ? " clusters" : "", pl.blocks, Cfg::NTHREADS,
+            (unsigned)Cfg::SMEM, p.n_seqs, p.max_q, p.Hq, p.Hkv);
+  if (!pl.cluster) {
+    paged_fwd_kernel<Cfg, false><<<(unsigned)pl.blocks, Cfg::NTHREADS, Cfg::SMEM, s>>>(tk, tv, p);
+    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  }
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = kPagedCluster;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)pl.blocks);
+  cfg.blockDim = dim3(Cfg::NTHREADS);
+  cfg.dynamicSmemBytes = Cfg::SMEM;
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_fwd_kernel<Cfg, true>, tk, tv, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 template <int D, bool E4M3>
 int launch_paged_size(const PagedParams& p, const PagedPlan& pl, const attn_kv_cache_t* c, DeviceState* st, cudaStream_t s) {
   switch (pl.size) {
-    case 0: return launch_paged_cfg<PagedCfgOf<D, E4M3, 0>>(p, pl.blocks, c, st, s);
-    case 1: return launch_paged_cfg<PagedCfgOf<D, E4M3, 1>>(p, pl.blocks, c, st, s);
-    case 2: return launch_paged_cfg<PagedCfgOf<D, E4M3, 2>>(p, pl.blocks, c, st, s);
-    default: return launch_paged_cfg<PagedCfgOf<D, E4M3, 3>>(p, pl.blocks, c, st, s);
+    case 0: return launch_paged_cfg<PagedCfgOf<D, E4M3, 0>>(p, pl, c, st, s);
+    case 1: return launch_paged_cfg<PagedCfgOf<D, E4M3, 1>>(p, pl, c, st, s);
+    case 2: return launch_paged_cfg<PagedCfgOf<D, E4M3, 2>>(p, pl, c, st, s);
+    default: return launch_paged_cfg<PagedCfgOf<D, E4M3, 3>>(p, pl, c, st, s);
   }
 }
 // A kernel that is launched while the one before it in the stream still runs and
@@ -259,7 +282,7 @@ template <int D>
 int launch_paged(const PagedParams& p, const PagedPlan& pl, const attn_kv_cache_t* c, DeviceState* st, cudaStream_t s) {
   const int rc = c->dtype == ATTN_FP8_E4M3 ? launch_paged_size<D, true>(p, pl, c, st, s)
                                            : launch_paged_size<D, false>(p, pl, c, st, s);
-  if (rc != ATTN_OK || p.max_kv <= pl.unit) return rc;  // (a segment of one unit is never shared)
+  if (rc != ATTN_OK || pl.cluster || p.max_kv <= pl.unit) return rc;  // (a segment of one unit is never shared)
   const long long blocks = ((long long)p.Tq * p.Hq + 7) / 8;
   ATTN_LOGF("attn: paged_combine_kernel<%d> grid=(%lld) block=256 Tq=%d Hq=%d\n", D, blocks, p.Tq, p.Hq);
   return launch_dependent(paged_combine_kernel<D>, blocks, 256, 0, s, p, pl.block_rows, pl.unit);
@@ -267,15 +290,14 @@ int launch_paged(const PagedParams& p, const PagedPlan& pl, const attn_kv_cache_
 
 // ---------------------------------------------------------------- packed sequences on tcgen05
 // The long-range configurations over packed sequences (1) or a paged cache (2
-// bf16, 3 e4m3).  Exponentials in software at d = 128 as there (4 x 4096 tokens
-// causal: 568 us without, 555 with), except over an e4m3 cache, whose expanding
-// warps need the issue slots, and at d = 64, where it gains nothing (the batch of
-// prompts up to 1024: 32.0 us without, 32.8 with).
+// bf16, 3 e4m3).  All exponentials on the hardware unit: the software share's 1e-4
+// would show in the LSE of a short sequence, and it loses a NaN score (4 x 4096
+// tokens of 32/8 heads, causal: 568 us, with the share 555).
 // The heads of a group are always stacked where the group divides the tile: a
 // block then covers fewer tokens, which wastes less of a causal block's diagonal
 // and of a short sequence, and a key tile is read once per group.
 template <bool C, int R> using CfgRagD64 = FwdCfg<64, 128, 2, 3, 3, C, false, 0, 1, false, 1, true, false, R>;
-template <bool C, int R> using CfgRagD128 = FwdCfg<128, 128, 2, 2, 2, C, false, R == 3 ? 0 : (C ? 2 : 1), 1, false, 1, true, false, R>;
+template <bool C, int R> using CfgRagD128 = FwdCfg<128, 128, 2, 2, 2, C, false, 0, 1, false, 1, true, false, R>;
 template <bool C, int R> using CfgRagD256 = FwdCfg<256, 64, 1, 2, 2, C, false, 0, 2, false, 1, true, false, R>;
 
 int ragged_block_rows(int d) { return d == 256 ? 128 : 256; }
@@ -655,8 +677,10 @@ int attn_fwd_paged(const void* q, const attn_kv_cache_t* cache, void* o, float* 
   if (cache->n_pages == 0) max_kv = 0;  // there is nothing to read
   const PagedPlan pl = paged_plan(cache, Tq, n_seqs, max_q, Hq, max_kv);
   const PagedSpace sp = paged_space(pl, Tq, n_seqs, Hq, d);
-  if (workspace == nullptr || workspace_bytes < sp.all()) return ATTN_ERR_INVALID_ARG;
-  if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
+  if (sp.all() > 0) {
+    if (workspace == nullptr || workspace_bytes < sp.all()) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
+  }
   int dev = 0;
   DeviceState* st = nullptr;
   if ((rc = device_state(&dev, &st)) != ATTN_OK) return rc;
@@ -733,6 +757,7 @@ int attn_fwd_paged(const void* q, const attn_kv_cache_t* cache, void* o, float* 
   p.n_pages = cache->n_pages;
   p.page_shift = page_shift(cache);
   p.causal = causal;
+  p.row_tiles = pl.row_tiles;
   p.sl2 = scale * 1.4426950408889634f;
   p.base = static_cast<long long*>(workspace);
   p.o_part = o_part;

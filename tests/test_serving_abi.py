@@ -130,7 +130,8 @@ def paged(c=None, **kw):
     (dict(causal=3), INVALID), (dict(scale=math.inf), INVALID), (dict(cq=None, Tq=3), INVALID),
     (dict(lens=None), INVALID), (dict(o=None), INVALID), (dict(table=None), INVALID), (dict(q=None), INVALID),
     (dict(q=P + 8), MISALIGNED), (dict(qs=516), MISALIGNED), (dict(o=P + 8), MISALIGNED), (dict(table=P + 2), MISALIGNED),
-    (dict(ws=None), INVALID), (dict(wsb=100), INVALID), (dict(ws=P + 4), MISALIGNED),
+    (dict(ws=None, width=400, max_kv=6400), INVALID), (dict(wsb=100, width=400, max_kv=6400), INVALID),
+    (dict(ws=P + 4, width=400, max_kv=6400), MISALIGNED),
     (dict(Tq=0), OK), (dict(n=0), OK), (dict(Hq=0), OK)])
 def test_paged_refusals(kw, status):
     assert paged(**kw) == status
@@ -140,8 +141,10 @@ def test_paged_workspace():
     f = ea.attn_fwd_paged_workspace_bytes
     c = cache(Hkv=8)
     assert f(c, 0, 1, 1, 32, 64) == 0 and f(c, 4, 4, 1, 33, 64) == -1 and f(c, 4, 4, 5, 32, 64) == -1
-    # a count per sequence, and two partial blocks of 8 rows for each of the 4 * 8 * 3 units of 64 keys
-    assert f(c, 4, 4, 1, 32, 192) == 256 + 2 * 96 * 8 * 128 * 4 + 2 * 96 * 8 * 4
+    assert f(c, 4, 4, 1, 32, 192) == 0  # a cluster of blocks per sequence and head
+    # a count per sequence, and two partial blocks of 8 rows for each of the 50 * 8 * 3 units, or
+    # of the 2 blocks that an SM holds where those are fewer
+    assert f(c, 50, 50, 1, 32, 192) == 512 + 2 * 296 * 8 * 128 * 4 + 2 * 296 * 8 * 4
     assert f(c, 64, 64, 1, 32, 1 << 17) == f(c, 64, 64, 1, 32, 1 << 20)  # the grid is bounded by the GPU
     # 300 tokens of 4 stacked heads: the item list; with long contexts windows join it
     items = (300 * 4 + 255) // 256
