@@ -12,7 +12,7 @@ namespace attn {
 // Packed sequences (one-block-per-item kernel, RAGGED configurations): the
 // work items come from a list in device memory (ragged_plan_kernel).
 struct RaggedParams {
-  const int* plan;   // number of items, then from int 8 on items of 8 ints: seq, block, q0, nq, k0, nk, 0, 0
+  const int* plan;   // items of 8 ints: seq (-1: none), block, q0, nq, k0, nk, 0, 0
   int max_items;     // items that the launch's grid has room for
   int Tq;            // query tokens in all (lse rows)
   const int* table;  // paged: page table [n_seqs, table_width]

@@ -92,9 +92,10 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
     const int bi = L / per, within = L - bi * per;
     const int bsz = p.nh - bi * p.band < p.band ? p.nh - bi * p.band : p.band;
     const int item = within / bsz;
-    if (item >= __ldcg(p.rg.plan)) return;  // (from L2: written while this grid was being launched)
-    const int4 i0 = __ldcg(reinterpret_cast<const int4*>(p.rg.plan) + 2 + 2 * item);
-    const int2 i1 = __ldcg(reinterpret_cast<const int2*>(p.rg.plan) + 6 + 4 * item);
+    // (from L2: the list was written while this grid was being launched)
+    const int4 i0 = __ldcg(reinterpret_cast<const int4*>(p.rg.plan) + 2 * item);
+    const int2 i1 = __ldcg(reinterpret_cast<const int2*>(p.rg.plan) + 2 + 4 * item);
+    if (i0.x < 0) return;
     hy = bi * p.band + within % bsz;
     b = 0;
     // (a shuffle from lane 0 shows the compiler that the warp agrees on them, so

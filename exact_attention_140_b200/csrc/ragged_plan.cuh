@@ -17,7 +17,6 @@ namespace attn {
 
 constexpr int kPlanThreads = 512;
 constexpr int kPlanBuckets = 256;
-constexpr int kPlanHead = 8;   // ints in front of the items
 constexpr int kPlanItem = 8;   // ints of an item
 
 struct PlanParams {
@@ -132,7 +131,7 @@ __global__ void __launch_bounds__(kPlanThreads) ragged_plan_kernel(const PlanPar
     for (int qb = lane; qb < nb; qb += 32) {
       const int at = atomicAdd(&s_hist[level(cost(qb, nq, nk))], 1);
       if (at < p.max_items) {
-        int4* it = reinterpret_cast<int4*>(p.plan + kPlanHead + kPlanItem * at);
+        int4* it = reinterpret_cast<int4*>(p.plan + kPlanItem * at);
         it[0] = make_int4(s, qb, q0, nq);
         it[1] = make_int4(k0, nk, 0, 0);
       } else {
@@ -140,7 +139,9 @@ __global__ void __launch_bounds__(kPlanThreads) ragged_plan_kernel(const PlanPar
       }
     }
   }
-  if (tid == 0) p.plan[0] = s_count < p.max_items ? s_count : p.max_items;
+  // the slots behind the last item say so themselves: a block of the attention
+  // kernel then needs one look
+  for (int i = s_count + tid; i < p.max_items; i += kPlanThreads) p.plan[kPlanItem * i] = -1;
   if (bad) atomicOr(p.err, kErrIndex);
 }
 

@@ -307,7 +307,7 @@ long long ragged_max_items(long long Tq, long long n_seqs, int Hq, int Hkv, int 
   const long long R = ragged_block_rows(d), n = n_seqs < Tq ? n_seqs : Tq;
   return (Tq * ragged_rows_per_token(Hq, Hkv) + n * (R - 1)) / R;
 }
-long long ragged_plan_bytes(long long items) { return (4 * (kPlanHead + kPlanItem * items) + 255) / 256 * 256; }
+long long ragged_plan_bytes(long long items) { return (4 * kPlanItem * items + 255) / 256 * 256; }
 
 struct RaggedCall {
   const void *q, *k, *v;

@@ -31,6 +31,10 @@ VARLEN = [  # Hq, Hkv, d, query lengths, key lengths (None: the same)
     (8, 2, 256, [3, 150], [400, 100]),
     (4, 1, 128, [256, 512], [1024, 512]),
     (16, 16, 128, [1] * 40, None),
+    (4, 2, 64, [37, 0, 5, 130] * 10, None),
+    (2, 2, 128, [3] * 128, [9] * 128),
+    (4, 4, 64, [2, 70, 0, 300, 1] * 60, None),
+    (8, 2, 128, [1, 33] * 70, [200, 33] * 70),
 ]
 
 

@@ -109,9 +109,9 @@ def test_varlen_workspace():
     f = ea.attn_fwd_varlen_workspace_bytes
     assert f(-1, 1, 4, 2, 128) == f(8, 1, 3, 2, 128) == f(8, 1, 4, 0, 128) == f(8, 1, 4, 2, 96) == -1
     assert f(0, 1, 4, 2, 128) == f(8, 0, 4, 2, 128) == 0
-    # a list of 32-byte items behind a 32-byte head: blocks of 256 rows, groups of 4 stacked
-    assert f(1000, 3, 32, 8, 128) == (32 + 32 * ((4000 + 3 * 255) // 256) + 255) // 256 * 256
-    assert f(1000, 3, 8, 8, 256) == (32 + 32 * ((1000 + 3 * 127) // 128) + 255) // 256 * 256
+    # a list of 32-byte items: blocks of 256 rows, groups of 4 stacked
+    assert f(1000, 3, 32, 8, 128) == (32 * ((4000 + 3 * 255) // 256) + 255) // 256 * 256
+    assert f(1000, 3, 8, 8, 256) == (32 * ((1000 + 3 * 127) // 128) + 255) // 256 * 256
     assert f(5, 100, 8, 8, 128) == f(5, 5, 8, 8, 128)  # at most a sequence per token
 
 
@@ -148,7 +148,7 @@ def test_paged_workspace():
     assert f(c, 64, 64, 1, 32, 1 << 17) == f(c, 64, 64, 1, 32, 1 << 20)  # the grid is bounded by the GPU
     # 300 tokens of 4 stacked heads: the item list; with long contexts windows join it
     items = (300 * 4 + 255) // 256
-    assert f(c, 300, 1, 300, 32, 500) == (32 + 32 * items + 255) // 256 * 256
+    assert f(c, 300, 1, 300, 32, 500) == (32 * items + 255) // 256 * 256
     assert f(c, 300, 1, 300, 32, 1 << 16) > 300 * 32 * 128 * 4 * 2
 
 
