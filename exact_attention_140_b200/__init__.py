@@ -379,12 +379,14 @@ def attn_fwd_paged(q, cache, o, lse, Tq, n_seqs, max_q, cu_q, table, table_width
 
 
 torch = None  # the torch module, from the first use of a wrapper below
+_bf16 = _f32 = _f64 = _i32 = _i64 = _u8 = None  # its types
 
 
 def _load_torch():
-    global torch
+    global torch, _bf16, _f32, _f64, _i32, _i64, _u8
     if torch is None:
         import torch as t
+        _bf16, _f32, _f64, _i32, _i64, _u8 = t.bfloat16, t.float32, t.float64, t.int32, t.int64, t.uint8
         torch = t
     return torch
 
@@ -415,22 +417,35 @@ def _on_current_device(*tensors):
 
 
 def _rows(x, name):
-    """Token stride of a bf16 [T, H, d] tensor whose heads are contiguous."""
-    if x.dtype is not _load_torch().bfloat16 or x.dim() != 3:
+    """(T, H, d, token stride) of a bf16 [T, H, d] tensor whose heads are contiguous."""
+    if torch is None:
+        _load_torch()
+    if x.dtype is not _bf16 or x.dim() != 3:
         raise TypeError(f"{name} must be a bf16 tensor [T, H, d]")
     T, H, d = x.shape
-    st = x.stride()
-    if (st[2] != 1 and d > 1) or (st[1] != d and H > 1):
-        if x.numel() > 0:
-            raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return st[0] if T > 1 else H * d
+    st, sh, sd = x.stride()
+    if ((sd != 1 and d > 1) or (sh != d and H > 1)) and x.numel() > 0:
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return T, H, d, st if T > 1 else H * d
 
 
-def _index(x, name, dtype, n=None, dim=1):
-    if x.dtype is not getattr(_load_torch(), dtype) or x.dim() != dim or not x.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous {dtype} tensor of {dim} dimension(s)")
-    if n is not None and x.shape[0] != n:
-        raise ValueError(f"{name} has {x.shape[0]} entries, {n} are needed")
+def _index(x, name, dtype, n=None):
+    """x is a contiguous 1-D tensor of the type, with n entries; returns their number."""
+    if x.dtype is not dtype or x.dim() != 1 or not x.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous 1-D {dtype} tensor")
+    m = x.shape[0]
+    if n is not None and m != n:
+        raise ValueError(f"{name} has {m} entries, {n} are needed")
+    return m
+
+
+def _table(x):
+    """(sequences, width) of a page table."""
+    if torch is None:
+        _load_torch()
+    if x.dtype is not _i32 or x.dim() != 2 or not x.is_contiguous():
+        raise TypeError("table must be a contiguous 2-D int32 tensor")
+    return x.shape
 
 
 def _use_stream(stream, dev, *new):
@@ -463,7 +478,7 @@ class Rope:
         _load_torch()
         _need(rot_dim == 0 or freqs is not None, "freqs are needed where rot_dim > 0")
         if freqs is not None and rot_dim > 0:
-            _index(freqs, "freqs", "float64", rot_dim // 2)
+            _index(freqs, "freqs", _f64, rot_dim // 2)
         d = None
         for w in (q_weight, k_weight):
             if w is not None:
@@ -503,11 +518,12 @@ class KVCache:
                                    self.page_size, self.Hkv, self.d, ATTN_FP8_E4M3 if e4m3 else ATTN_BF16)
 
 
-def _check_rope_use(rope, d, positions, T):
+def _check_rope_use(rope, d, positions, T, dev):
     _need(rope.d is None or rope.d == d, "the norm weights are for another head size")
     if rope.rot_dim > 0:
         _need(positions is not None, "positions are needed where rot_dim > 0")
-        _index(positions, "positions", "int64", T)
+        _index(positions, "positions", _i64, T)
+    _handle_device(rope, dev)
 
 
 def _handle_device(handle, dev):
@@ -516,32 +532,35 @@ def _handle_device(handle, dev):
 
 
 def _like(x):
-    """A new contiguous tensor like x."""
-    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+    """A new contiguous tensor of x's shape."""
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
+def _out_rows(out, like, name):
+    """Token stride of a given output tensor that must have the shape of `like`."""
+    _need(out.shape == like.shape, f"{name} must have its input's shape")
+    return _rows(out, name)[3]
 
 
 def qk_norm_rope(q, k, positions, rope, q_out=None, k_out=None, stream=None):
     """q [T, Hq, d] and k [T, Hkv, d] (bf16, slices of a fused projection allowed) normed and rotated;
     returns (q_out, k_out), new contiguous tensors unless given (q_out=q and k_out=k work in place)."""
-    qs, ks = _rows(q, "q"), _rows(k, "k")
-    T, Hq, d = q.shape
-    Tk, Hkv, dk = k.shape
+    T, Hq, d, qs = _rows(q, "q")
+    Tk, Hkv, dk, ks = _rows(k, "k")
     _need(Tk == T and dk == d, "q and k must have the same tokens and head size")
-    _check_rope_use(rope, d, positions, T)
     dev = _on_current_device(q, k, positions, q_out, k_out)
-    _handle_device(rope, dev)
+    _check_rope_use(rope, d, positions, T, dev)
     new_q = new_k = None
-    qos, kos = Hq * d, Hkv * d
     if q_out is None:
         q_out = new_q = _like(q)
+        qos = Hq * d
     else:
-        _need(q_out.shape == q.shape, "q_out must have q's shape")
-        qos = _rows(q_out, "q_out")
+        qos = _out_rows(q_out, q, "q_out")
     if k_out is None:
         k_out = new_k = _like(k)
+        kos = Hkv * d
     else:
-        _need(k_out.shape == k.shape, "k_out must have k's shape")
-        kos = _rows(k_out, "k_out")
+        kos = _out_rows(k_out, k, "k_out")
     rc = _lib.attn_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), T, Hq, Hkv, d, qs, ks,
                                 qos, kos, _ptr(positions), rope.struct, _use_stream(stream, dev, new_q, new_k))
     if rc:
@@ -552,30 +571,27 @@ def qk_norm_rope(q, k, positions, rope, q_out=None, k_out=None, stream=None):
 def kv_write(cache, k, v, slots, q=None, positions=None, rope=None, q_out=None, stream=None):
     """Keys and values [T, Hkv, d] (bf16) into the cache's slots (int64 [T], negative: skipped).  With rope the
     keys are normed and rotated on the way, and so are the queries q [T, Hq, d], which are returned."""
-    ks, vs = _rows(k, "k"), _rows(v, "v")
-    T = k.shape[0]
-    _need(k.shape == v.shape == (T, cache.Hkv, cache.d), "k and v must be [T, Hkv, d] of the cache")
-    _index(slots, "slots", "int64", T)
+    T, Hkv, d, ks = _rows(k, "k")
+    Tv, Hv, dv, vs = _rows(v, "v")
+    _need(T == Tv and Hkv == Hv == cache.Hkv and d == dv == cache.d, "k and v must be [T, Hkv, d] of the cache")
+    _index(slots, "slots", _i64, T)
     _need(rope is not None or q is None, "queries only take part where rope is given")
     dev = _on_current_device(k, v, slots, q, positions, q_out)
     _handle_device(cache, dev)
     rs = None
     if rope is not None:
-        _check_rope_use(rope, cache.d, positions, T)
-        _handle_device(rope, dev)
+        _check_rope_use(rope, d, positions, T, dev)
         rs = rope.struct
     Hq = qs = qos = 0
     new = None
     if q is not None:
-        qs = _rows(q, "q")
-        Hq = q.shape[1]
-        _need(q.shape[0] == T and q.shape[2] == cache.d, "q must have k's tokens and head size")
+        Tq, Hq, dq, qs = _rows(q, "q")
+        _need(Tq == T and dq == d, "q must have k's tokens and head size")
         if q_out is None:
             q_out = new = _like(q)
-            qos = Hq * cache.d
+            qos = Hq * d
         else:
-            _need(q_out.shape == q.shape, "q_out must have q's shape")
-            qos = _rows(q_out, "q_out")
+            qos = _out_rows(q_out, q, "q_out")
     rc = _lib.attn_kv_write(cache.struct, k.data_ptr(), v.data_ptr(), T, ks, vs, slots.data_ptr(), rs, _ptr(positions),
                             _ptr(q), _ptr(q_out), Hq, qs, qos, _use_stream(stream, dev, new))
     if rc:
@@ -586,45 +602,38 @@ def kv_write(cache, k, v, slots, q=None, positions=None, rope=None, q_out=None, 
 def kv_read(cache, table, cu, T, k_out=None, v_out=None, stream=None):
     """The cached tokens of each sequence (pages table[s], int32; boundaries cu of the T output rows, int32
     [n_seqs + 1]) as packed bf16 keys and values [T, Hkv, d]."""
-    _index(table, "table", "int32", dim=2)
-    n, width = table.shape
-    _index(cu, "cu", "int32", n + 1)
+    n, width = _table(table)
+    _index(cu, "cu", _i32, n + 1)
     dev = _on_current_device(table, cu, k_out, v_out)
     _handle_device(cache, dev)
     shape = (T, cache.Hkv, cache.d)
-    new = []
+    new_k = new_v = None
     for t in (k_out, v_out):
-        _need(t is None or (t.shape == shape and t.dtype is torch.bfloat16 and t.is_contiguous()),
+        _need(t is None or (t.shape == shape and t.dtype is _bf16 and t.is_contiguous()),
               "k_out and v_out must be contiguous bf16 [T, Hkv, d]")
     if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=table.device)
-        new.append(k_out)
+        k_out = new_k = table.new_empty(shape, dtype=_bf16)
     if v_out is None:
-        v_out = torch.empty_like(k_out)
-        new.append(v_out)
+        v_out = new_v = torch.empty_like(k_out)
     rc = _lib.attn_kv_read(cache.struct, table.data_ptr(), width, cu.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(), T,
-                           _use_stream(stream, dev, *new))
+                           _use_stream(stream, dev, new_k, new_v))
     if rc:
         raise AttnError(rc, "attn_kv_read")
     return k_out, v_out
 
 
-def _outputs(q, o, lse, return_lse):
-    """(o, lse, tensors made here)"""
-    T, H, _ = q.shape
-    new = []
+def _outputs(q, T, H, o, lse, return_lse):
+    """(o, lse, the ones that were made here)"""
+    new_o = new_lse = None
     if o is None:
-        o = _like(q)
-        new.append(o)
+        o = new_o = _like(q)
     else:
-        _need(o.shape == q.shape and o.dtype is torch.bfloat16 and o.is_contiguous(), "o must be contiguous bf16 like q")
+        _need(o.shape == q.shape and o.dtype is _bf16 and o.is_contiguous(), "o must be contiguous bf16 like q")
     if lse is not None:
-        _need(lse.shape == (H, T) and lse.dtype is torch.float32 and lse.is_contiguous(),
-              "lse must be contiguous fp32 [Hq, T]")
+        _need(lse.shape == (H, T) and lse.dtype is _f32 and lse.is_contiguous(), "lse must be contiguous fp32 [Hq, T]")
     elif return_lse:
-        lse = q.new_empty((H, T), dtype=torch.float32)
-        new.append(lse)
-    return o, lse, new
+        lse = new_lse = q.new_empty((H, T), dtype=_f32)
+    return o, lse, new_o, new_lse
 
 
 def attention_varlen(q, k, v, cu_q, cu_k, causal: bool = False, scale: float | None = None, return_lse: bool = True,
@@ -632,24 +641,20 @@ def attention_varlen(q, k, v, cu_q, cu_k, causal: bool = False, scale: float | N
     """O [Tq, Hq, d] (and LSE [Hq, Tq]) of packed sequences: q [Tq, Hq, d], k/v [Tk, Hkv, d] (bf16, slices of a
     fused projection allowed), boundaries cu_q, cu_k int32 [n_seqs + 1].  Rows outside every sequence are
     not written."""
-    qs, ks, vs = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
-    Tq, Hq, d = q.shape
-    Tk, Hkv, dk = k.shape
-    _need(k.shape == v.shape and dk == d, "k and v must have the same shape, and q's head size")
-    _index(cu_q, "cu_q", "int32")
-    n = cu_q.shape[0] - 1
-    _index(cu_k, "cu_k", "int32", n + 1)
+    Tq, Hq, d, qs = _rows(q, "q")
+    Tk, Hkv, dk, ks = _rows(k, "k")
+    Tv, Hv, dv, vs = _rows(v, "v")
+    _need(Tv == Tk and Hv == Hkv and dv == dk == d, "k and v must have the same shape, and q's head size")
+    n = _index(cu_q, "cu_q", _i32) - 1
+    _index(cu_k, "cu_k", _i32, n + 1)
     dev = _on_current_device(q, k, v, cu_q, cu_k, o, lse)
-    o, lse, new = _outputs(q, o, lse, return_lse)
+    o, lse, new_o, new_lse = _outputs(q, Tq, Hq, o, lse, return_lse)
     nbytes = _lib.attn_fwd_varlen_workspace_bytes(Tq, n, Hq, Hkv, d)
-    ws = None
-    if nbytes > 0:
-        ws = q.new_empty(nbytes // 2 + 1)  # (bf16 elements)
-        new.append(ws)
+    ws = q.new_empty(nbytes // 2) if nbytes > 0 else None  # (bf16 elements; the sizes are multiples of 256)
     rc = _lib.attn_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(lse), Tq, Tk, n,
-                              cu_q.data_ptr(), cu_k.data_ptr(), Hq, Hkv, d, qs, ks, vs, int(causal),
-                              1.0 / math.sqrt(d) if scale is None else scale, _ptr(ws), max(nbytes, 0),
-                              _use_stream(stream, dev, *new))
+                              cu_q.data_ptr(), cu_k.data_ptr(), Hq, Hkv, d, qs, ks, vs, 1 if causal else 0,
+                              d ** -0.5 if scale is None else scale, _ptr(ws), nbytes if nbytes > 0 else 0,
+                              _use_stream(stream, dev, new_o, new_lse, ws))
     if rc:
         raise AttnError(rc, "attn_fwd_varlen")
     return (o, lse) if return_lse else o
@@ -660,14 +665,12 @@ def attention_paged(q, cache, table, kv_lens, cu_q=None, max_q=None, max_kv=None
     """O [Tq, Hq, d] (and LSE [Hq, Tq]) of new tokens q over the cache, which holds them already: table int32
     [n_seqs, width], kv_lens int32 [n_seqs] with the new tokens counted.  cu_q int32 [n_seqs + 1] gives the
     sequences' rows of q and max_q bounds their number; without cu_q every sequence has Tq / n_seqs rows."""
-    qs = _rows(q, "q")
-    Tq, Hq, d = q.shape
+    Tq, Hq, d, qs = _rows(q, "q")
     _need(d == cache.d, "q and the cache differ in head size")
-    _index(table, "table", "int32", dim=2)
-    n, width = table.shape
-    _index(kv_lens, "kv_lens", "int32", n)
+    n, width = _table(table)
+    _index(kv_lens, "kv_lens", _i32, n)
     if cu_q is not None:
-        _index(cu_q, "cu_q", "int32", n + 1)
+        _index(cu_q, "cu_q", _i32, n + 1)
         max_q = Tq if max_q is None else min(max_q, Tq)
     else:
         _need(n > 0 and Tq % n == 0 and max_q in (None, Tq // n), "without cu_q every sequence has Tq / n_seqs rows")
@@ -676,16 +679,13 @@ def attention_paged(q, cache, table, kv_lens, cu_q=None, max_q=None, max_kv=None
         max_kv = width * cache.page_size
     dev = _on_current_device(q, table, kv_lens, cu_q, o, lse)
     _handle_device(cache, dev)
-    o, lse, new = _outputs(q, o, lse, return_lse)
+    o, lse, new_o, new_lse = _outputs(q, Tq, Hq, o, lse, return_lse)
     nbytes = _lib.attn_fwd_paged_workspace_bytes(cache.struct, Tq, n, max_q, Hq, max_kv)
-    ws = None
-    if nbytes > 0:
-        ws = q.new_empty(nbytes // 2 + 1)  # (bf16 elements)
-        new.append(ws)
+    ws = q.new_empty(nbytes // 2) if nbytes > 0 else None  # (bf16 elements; the sizes are multiples of 256)
     rc = _lib.attn_fwd_paged(q.data_ptr(), cache.struct, o.data_ptr(), _ptr(lse), Tq, n, max_q, _ptr(cu_q),
-                             table.data_ptr(), width, kv_lens.data_ptr(), max_kv, Hq, qs, int(causal),
-                             1.0 / math.sqrt(d) if scale is None else scale, _ptr(ws), max(nbytes, 0),
-                             _use_stream(stream, dev, *new))
+                             table.data_ptr(), width, kv_lens.data_ptr(), max_kv, Hq, qs, 1 if causal else 0,
+                             d ** -0.5 if scale is None else scale, _ptr(ws), nbytes if nbytes > 0 else 0,
+                             _use_stream(stream, dev, new_o, new_lse, ws))
     if rc:
         raise AttnError(rc, "attn_fwd_paged")
     return (o, lse) if return_lse else o

@@ -219,8 +219,8 @@ def test_binding_checks():
     with pytest.raises(ValueError):
         ea._rows(torch.zeros(3, 64, 2, **bf).transpose(1, 2), "x")
     x = torch.zeros(5, 6, 64, **bf)
-    assert ea._rows(x[:, 1:3], "x") == 384 and ea._rows(x[:1, 1:3], "x") == 128
+    assert ea._rows(x[:, 1:3], "x") == (5, 2, 64, 384) and ea._rows(x[:1, 1:3], "x") == (1, 2, 64, 128)
     with pytest.raises(TypeError):
-        ea._index(torch.zeros(3), "x", "int32")
+        ea._index(torch.zeros(3), "x", torch.int32)
     with pytest.raises(ValueError):
-        ea._index(torch.zeros(3, dtype=torch.int32), "x", "int32", 4)
+        ea._index(torch.zeros(3, dtype=torch.int32), "x", torch.int32, 4)
