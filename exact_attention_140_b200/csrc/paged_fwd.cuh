@@ -934,44 +934,76 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
 // One output row from S partial rows, by a warp: part w is row slot(w) of o_part
 // (fp32, normalised by its own sum) with its LSE (natural log) in lse_part.
 //   LSE = ln sum_w exp(LSE_w),   O = sum_w exp(LSE_w - LSE) O_w
-// (parts without a visible key have LSE_w = -inf and weigh nothing.)  Bound by the
-// latency of a few reads from L2: eight parts' rows are requested together.
+// (parts without a visible key have O_w = 0, LSE_w = -inf and weigh nothing.)  Bound
+// by the latency of one read from L2: the first eight parts' rows and all parts'
+// LSE are requested together, and the row of a lane is one wide load.
 template <int D, class Slot>
 __device__ __forceinline__ void merge_parts(const float* o_part, const float* lse_part, int S, Slot slot, int lane,
                                             __nv_bfloat16* o, float* lse) {
   constexpr int PER = D / 32;
-  float mx = -INFINITY;
-  for (int w = lane; w < S; w += 32) mx = fmaxf(mx, __ldcg(lse_part + slot(w)));
+  struct Piece { float v[PER]; };
+  auto fetch = [&](int w) -> Piece {
+    Piece x;
+    const float* src = o_part + slot(w) * D + PER * lane;
+    if constexpr (PER == 2) {
+      const float2 a = __ldcg(reinterpret_cast<const float2*>(src));
+      x.v[0] = a.x;
+      x.v[1] = a.y;
+    } else {
+#pragma unroll
+      for (int e = 0; e < PER; e += 4) {
+        const float4 a = __ldcg(reinterpret_cast<const float4*>(src + e));
+        x.v[e] = a.x;
+        x.v[e + 1] = a.y;
+        x.v[e + 2] = a.z;
+        x.v[e + 3] = a.w;
+      }
+    }
+    return x;
+  };
+  constexpr int AHEAD = 8;
+  Piece y[AHEAD];
+  float ls = lane < S ? __ldcg(lse_part + slot(lane)) : -INFINITY;
+#pragma unroll
+  for (int u = 0; u < AHEAD; ++u) {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) y[u].v[e] = 0.f;
+    if (u < S) y[u] = fetch(u);
+  }
+  float mx = ls;
+  for (int w = 32 + lane; w < S; w += 32) mx = fmaxf(mx, __ldcg(lse_part + slot(w)));
 #pragma unroll
   for (int i = 16; i > 0; i >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
   const float mu = mx == -INFINITY ? 0.f : mx;
   float acc[PER], wsum = 0.f;
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  for (int w0 = 0; w0 < S; w0 += 32) {
-    const float wl = w0 + lane < S ? expf(__ldcg(lse_part + slot(w0 + lane)) - mu) : 0.f;
-    const int n = S - w0 < 32 ? S - w0 : 32;
-    for (int j0 = 0; j0 < n; j0 += 8) {
-      float wt[8], y[8][PER];
+  for (int w0 = 0; w0 < S; w0 += AHEAD) {
+    if (w0 > 0) {
+      if (w0 % 32 == 0) ls = w0 + lane < S ? __ldcg(lse_part + slot(w0 + lane)) : -INFINITY;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        wt[u] = __shfl_sync(0xffffffffu, wl, (j0 + u) & 31);
-        const bool live = j0 + u < n && wt[u] != 0.f;  // uniform across the warp
+      for (int u = 0; u < AHEAD; ++u)
+        if (w0 + u < S) y[u] = fetch(w0 + u);
+    }
+    const float wl = expf(ls - mu);  // (0 behind the last part)
 #pragma unroll
-        for (int e = 0; e < PER; ++e) y[u][e] = live ? __ldcg(o_part + slot(w0 + j0 + u) * D + 32 * e + lane) : 0.f;
-        if (!live) wt[u] = 0.f;
-      }
+    for (int u = 0; u < AHEAD; ++u) {
+      const float wt = __shfl_sync(0xffffffffu, wl, (w0 + u) & 31);
+      if (w0 + u < S) {
+        wsum += wt;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        wsum += wt[u];
-#pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] = fmaf(wt[u], y[u][e], acc[e]);
+        for (int e = 0; e < PER; ++e) acc[e] = wt == 0.f ? acc[e] : fmaf(wt, y[u].v[e], acc[e]);
       }
     }
   }
   const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+  uint32_t out[PER / 2];
 #pragma unroll
-  for (int e = 0; e < PER; ++e) o[32 * e + lane] = __float2bfloat16_rn(acc[e] * inv);
+  for (int e = 0; e < PER / 2; ++e) out[e] = ptx::pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  __nv_bfloat16* dst = o + PER * lane;
+  if constexpr (PER == 2) *reinterpret_cast<uint32_t*>(dst) = out[0];
+  if constexpr (PER == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+  if constexpr (PER == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
   if (lane == 0 && lse != nullptr) *lse = wsum == 0.f ? -INFINITY : mu + logf(wsum);
 }
 
@@ -979,26 +1011,52 @@ __device__ __forceinline__ void merge_parts(const float* o_part, const float* ls
 // The row's segment lies in the units [a, b), so in the blocks a / share ..
 // (b - 1) / share; each wrote a partial row (slot 1: its segment goes on in the
 // next block, slot 0: it ends here), and one block alone wrote the result itself.
+// What the attention kernel was given is looked up while that still runs, the
+// units in front of the sequence too where a warp counts them in one step
+// (`blocks` blocks shared all units); with more sequences they are read back.
+constexpr int kCombineCount = 64;  // sequences that a warp counts itself
 template <int D>
-__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p, int block_rows, int unit) {
-  ptx::grid_dep_wait();
+__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p, int block_rows, int unit, int blocks) {
   const long long i = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (i >= (long long)p.Tq * p.Hq) return;
-  const int t = (int)(i / p.Hq), h = (int)(i - (long long)t * p.Hq);
+  const int t = (int)(i / p.Hq), h = (int)(i - (long long)t * p.Hq), lane = threadIdx.x & 31;
   SeqRange sr;
-  const int s = paged_seq_of(p, t, sr);
-  if (s < 0) return;
+  const int s = t < p.Tq ? paged_seq_of(p, t, sr) : -1;
+  if (s < 0) {
+    ptx::grid_dep_wait();  // (on every path: the grid must not end before the one it follows)
+    return;
+  }
   const int g = p.group, units = paged_shape(sr, g, block_rows, unit).units;
   const long long pr = (long long)(t - sr.q0) * g + h % g;
   const int r = (int)(pr % block_rows);
-  const long long share = __ldcg(p.base + p.n_seqs);
-  const long long a = __ldcg(p.base + s) + ((pr / block_rows) * p.Hkv + h / g) * units;
-  const long long i0 = a / share, i1 = (a + units - 1) / share;
+  const long long in_seq = ((pr / block_rows) * p.Hkv + h / g) * units;
+  long long share, base;
+  if (p.n_seqs <= kCombineCount) {
+    long long total = 0, front = 0;
+    for (int x = lane; x < p.n_seqs; x += 32) {
+      const PagedShape sh = paged_shape(paged_seq(p, x), g, block_rows, unit);
+      const long long n = (long long)sh.row_tiles * p.Hkv * sh.units;
+      total += n;
+      front += x < s ? n : 0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      total += __shfl_xor_sync(0xffffffffu, total, o);
+      front += __shfl_xor_sync(0xffffffffu, front, o);
+    }
+    share = (total + blocks - 1) / blocks;
+    base = front;
+    ptx::grid_dep_wait();
+  } else {
+    ptx::grid_dep_wait();
+    share = __ldcg(p.base + p.n_seqs);
+    base = __ldcg(p.base + s);
+  }
+  const long long a = base + in_seq, i0 = a / share, i1 = (a + units - 1) / share;
   if (i0 == i1) return;
   const int S = (int)(i1 - i0 + 1);
   merge_parts<D>(p.o_part, p.lse_part, S,
-                 [&](int w) -> long long { return (2 * (i0 + w) + (w == S - 1 ? 0 : 1)) * block_rows + r; },
-                 threadIdx.x & 31, p.o + i * D, p.lse != nullptr ? p.lse + (long long)h * p.Tq + t : nullptr);
+                 [&](int w) -> long long { return (2 * (i0 + w) + (w == S - 1 ? 0 : 1)) * block_rows + r; }, lane,
+                 p.o + i * D, p.lse != nullptr ? p.lse + (long long)h * p.Tq + t : nullptr);
 }
 
 // Merge of the key windows of the tcgen05 kernel's items, parts
@@ -1011,12 +1069,12 @@ struct WindowParams : PagedSeqs {
 };
 template <int D>
 __global__ void __launch_bounds__(256) window_combine_kernel(const WindowParams p) {
-  ptx::grid_dep_wait();
   const long long i = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (i >= (long long)p.Tq * p.Hq) return;
   const int t = (int)(i / p.Hq), h = (int)(i - (long long)t * p.Hq);
   SeqRange sr;
-  if (paged_seq_of(p, t, sr) < 0 || sr.len <= p.window) return;
+  const bool several = t < p.Tq && paged_seq_of(p, t, sr) >= 0 && sr.len > p.window;
+  ptx::grid_dep_wait();
+  if (!several) return;
   const long long all = (long long)p.Tq * p.Hq;
   merge_parts<D>(p.o_part, p.lse_part, (sr.len + p.window - 1) / p.window,
                  [&](int w) -> long long { return w * all + i; }, threadIdx.x & 31, p.o + i * D,

@@ -285,7 +285,7 @@ int launch_paged(const PagedParams& p, const PagedPlan& pl, const attn_kv_cache_
   if (rc != ATTN_OK || pl.cluster || p.max_kv <= pl.unit) return rc;  // (a segment of one unit is never shared)
   const long long blocks = ((long long)p.Tq * p.Hq + 7) / 8;
   ATTN_LOGF("attn: paged_combine_kernel<%d> grid=(%lld) block=256 Tq=%d Hq=%d\n", D, blocks, p.Tq, p.Hq);
-  return launch_dependent(paged_combine_kernel<D>, blocks, 256, 0, s, p, pl.block_rows, pl.unit);
+  return launch_dependent(paged_combine_kernel<D>, blocks, 256, 0, s, p, pl.block_rows, pl.unit, pl.blocks);
 }
 
 // ---------------------------------------------------------------- packed sequences on tcgen05
