@@ -214,7 +214,10 @@ __global__ void __launch_bounds__(256, kHeadRowsBps) head_rows_kernel(const Head
   }
 }
 
+// Output rows: packed sequences (cu), or sequence s at rows s * stride .. (lens).
 struct KvReadParams {
+  const int* lens;  // with stride: tokens of each sequence, clamped to it
+  int stride;
   const void *k_pages, *v_pages;
   const unsigned char *k_exp, *v_exp;
   int n_pages, page_shift, Hkv, n_seqs, table_width;
@@ -234,13 +237,21 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const KvReadParams p) {
   const long long t = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (t >= p.T) return;
-  int lo = 0, hi = p.n_seqs;  // the last s with cu[s] <= t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if ((long long)__ldg(p.cu + mid) <= t) lo = mid; else hi = mid - 1;
+  int lo = 0;  // the token's sequence
+  long long start;
+  if (p.stride > 0) {
+    lo = (int)(t / p.stride);
+    start = (long long)lo * p.stride;
+    if (t - start >= __ldg(p.lens + lo)) return;
+  } else {
+    int hi = p.n_seqs;  // the last s with cu[s] <= t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if ((long long)__ldg(p.cu + mid) <= t) lo = mid; else hi = mid - 1;
+    }
+    start = __ldg(p.cu + lo);
+    if (lo >= p.n_seqs || start > t) return;  // behind the last sequence, or in front of the first
   }
-  const int start = __ldg(p.cu + lo);
-  if (lo >= p.n_seqs || start > t) return;  // behind the last sequence, or in front of the first
   const long long pos = t - start, pi = pos >> p.page_shift;
   int page = -1;
   if (start >= 0 && pi < p.table_width) page = __ldg(p.table + (long long)lo * p.table_width + pi);

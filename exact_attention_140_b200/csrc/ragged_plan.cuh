@@ -25,7 +25,8 @@ struct PlanParams {
   int n_seqs, Tq, Tk, max_q, max_kv;
   const int* cu_q;     // or nullptr: sequence s has the rows [s * max_q, (s + 1) * max_q)
   const int* cu_k;     // packed keys; nullptr: paged
-  const int* kv_lens;  // paged
+  const int* kv_lens;  // paged, or (k_stride > 0) packed with sequence s at k_stride * s
+  int k_stride;
   int rows_per_token;  // packed rows of a token (1 or the group size)
   int block_rows, bn;
   bool causal;
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(kPlanThreads) ragged_plan_kernel(const PlanPar
       k0 = k.x;
       nk = k.y - k.x;
     } else {
-      k0 = 0;
+      k0 = s * p.k_stride;
       nk = __ldg(p.kv_lens + s);
       if (nk < 0 || nk > p.max_kv) {
         bad = true;

@@ -107,16 +107,40 @@ int launch_kv_read(const KvReadParams& p, cudaStream_t s) {
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+int launch_kv_read_cache(KvReadParams& p, const attn_kv_cache_t* cache, const int* table, int table_width, int n_seqs,
+                         void* k, void* v, DeviceState* st, cudaStream_t s) {
+  p.k_pages = cache->k_pages;
+  p.v_pages = cache->v_pages;
+  p.k_exp = cache->k_exp;
+  p.v_exp = cache->v_exp;
+  p.n_pages = cache->n_pages;
+  p.page_shift = page_shift(cache);
+  p.Hkv = cache->Hkv;
+  p.n_seqs = n_seqs;
+  p.table_width = table_width;
+  p.table = table;
+  p.k = static_cast<__nv_bfloat16*>(k);
+  p.v = static_cast<__nv_bfloat16*>(v);
+  p.err = st->err;
+  const bool e4m3 = cache->dtype == ATTN_FP8_E4M3;
+  switch (cache->d) {
+    case 64: return e4m3 ? launch_kv_read<64, true>(p, s) : launch_kv_read<64, false>(p, s);
+    case 128: return e4m3 ? launch_kv_read<128, true>(p, s) : launch_kv_read<128, false>(p, s);
+    default: return e4m3 ? launch_kv_read<256, true>(p, s) : launch_kv_read<256, false>(p, s);
+  }
+}
+
 // ---------------------------------------------------------------- paged attention
 // How a paged call runs.  Few rows per sequence: paged_fwd_kernel, `size` its
 // block configuration, `blocks` its grid.  More (items > 0): the tcgen05 kernel
 // over listed items, each sequence's keys cut into n_windows windows where the
-// items are too few for the GPU.
+// items are too few for the GPU.  expand > 0: an e4m3 cache read back into bf16
+// rows first, `expand` of them for each sequence.
 struct PagedPlan {
   int size, block_rows, unit, row_tiles, blocks;
   bool cluster;
   long long items;
-  int window, n_windows;
+  int window, n_windows, expand;
 };
 long long ragged_max_items(long long Tq, long long n_seqs, int Hq, int Hkv, int d);
 int ragged_block_rows(int d);
@@ -149,6 +173,8 @@ PagedGeometry paged_geometry(int d, bool e4m3, int size) {
   }
 }
 
+constexpr long long kExpandBytes = 1ll << 30;  // of workspace for expanded keys and values, at most
+
 PagedPlan paged_plan(const attn_kv_cache_t* c, int Tq, int n_seqs, int max_q, int Hq, int max_kv) {
   PagedPlan pl = {};
   const int Hkv = c->Hkv;
@@ -174,6 +200,17 @@ PagedPlan paged_plan(const attn_kv_cache_t* c, int Tq, int n_seqs, int max_q, in
     const long long w = (((long long)max_kv + want - 1) / want + 127) / 128 * 128;
     pl.window = (int)(w < 128 ? 128 : w);
     pl.n_windows = max_kv > pl.window ? (int)(((long long)max_kv + pl.window - 1) / pl.window) : 1;
+    // Codes expanded once for all query blocks, or by every block for itself, by the
+    // rows of a sequence.  Measured on 4 sequences of up to 8192 keys, us by blocks /
+    // with the pass: d = 128 (32/8 heads) 512 rows 114 / 128, 1024 rows 182 / 179,
+    // 4096 rows 464 / 394; d = 256 (16/8) 256 rows 167 / 170, 512 rows 297 / 230;
+    // d = 64 (12/12) 2048 rows 237 / 261.  2048 tokens over 32768 of 32/8 x 128: 1339 /
+    // 1029.
+    const int expand_from = c->d == 64 ? INT_MAX : (c->d == 128 ? 1024 : 512);
+    const long long pad = ((long long)max_kv + 127) / 128 * 128;
+    if (c->dtype == ATTN_FP8_E4M3 && rows >= expand_from &&
+        n_seqs * pad * Hkv * c->d * 4 <= kExpandBytes && n_seqs * pad <= 0x7FFFFFFFll)
+      pl.expand = (int)pad;
     return pl;
   }
   while (pl.size < kPagedSizes - 1 && paged_block_rows(c->d, pl.size) < rows) ++pl.size;
@@ -195,10 +232,10 @@ PagedPlan paged_plan(const attn_kv_cache_t* c, int Tq, int n_seqs, int max_q, in
 // Workspace.  paged_fwd_kernel: a long long per sequence and one, the partial
 // rows, their LSE (nothing for clusters).  tcgen05: the item list, the windows' partial rows, their LSE.
 struct PagedSpace {
-  long long head, o, lse;  // bytes of each
-  long long all() const { return head + o + lse; }
+  long long head, o, lse, kv;  // bytes of each (kv: keys, and as much again for values)
+  long long all() const { return head + o + lse + 2 * kv; }
 };
-PagedSpace paged_space(const PagedPlan& pl, long long Tq, long long n_seqs, long long Hq, long long d) {
+PagedSpace paged_space(const PagedPlan& pl, long long Tq, long long n_seqs, long long Hq, long long Hkv, long long d) {
   auto round = [](long long b) { return (b + 255) / 256 * 256; };
   PagedSpace s = {};
   if (pl.items > 0) {
@@ -207,6 +244,7 @@ PagedSpace paged_space(const PagedPlan& pl, long long Tq, long long n_seqs, long
       s.o = round(pl.n_windows * Tq * Hq * d * 4);
       s.lse = round(pl.n_windows * Tq * Hq * 4);
     }
+    s.kv = n_seqs * pl.expand * Hkv * d * 2;
     return s;
   }
   if (pl.cluster) return s;
@@ -316,6 +354,7 @@ struct RaggedCall {
   int Tq, Tk, n_seqs, max_q, Hq, Hkv, d;
   const int *cu_q, *cu_k, *kv_lens, *table;
   int table_width, max_kv;
+  int seq_stride;  // packed keys whose sequence s starts at row s * seq_stride (kv_lens of them)
   long long q_stride, k_stride, v_stride;
   const attn_kv_cache_t* cache;  // paged
   bool causal;
@@ -366,6 +405,7 @@ int launch_ragged(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
   pp.cu_q = c.cu_q;
   pp.cu_k = c.cu_k;
   pp.kv_lens = c.kv_lens;
+  pp.k_stride = c.seq_stride;
   pp.rows_per_token = g;
   pp.block_rows = Cfg::BM * Cfg::NQT;
   pp.bn = Cfg::BN;
@@ -569,29 +609,10 @@ int attn_kv_read(const attn_kv_cache_t* cache, const int* table, int table_width
   int dev = 0;
   DeviceState* st = nullptr;
   if ((rc = device_state(&dev, &st)) != ATTN_OK) return rc;
-  KvReadParams p;
-  p.k_pages = cache->k_pages;
-  p.v_pages = cache->v_pages;
-  p.k_exp = cache->k_exp;
-  p.v_exp = cache->v_exp;
-  p.n_pages = cache->n_pages;
-  p.page_shift = page_shift(cache);
-  p.Hkv = cache->Hkv;
-  p.n_seqs = n_seqs;
-  p.table_width = table_width;
-  p.table = table;
+  KvReadParams p = {};
   p.cu = cu;
-  p.k = static_cast<__nv_bfloat16*>(k);
-  p.v = static_cast<__nv_bfloat16*>(v);
   p.T = T;
-  p.err = st->err;
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool e4m3 = cache->dtype == ATTN_FP8_E4M3;
-  switch (cache->d) {
-    case 64: return e4m3 ? launch_kv_read<64, true>(p, s) : launch_kv_read<64, false>(p, s);
-    case 128: return e4m3 ? launch_kv_read<128, true>(p, s) : launch_kv_read<128, false>(p, s);
-    default: return e4m3 ? launch_kv_read<256, true>(p, s) : launch_kv_read<256, false>(p, s);
-  }
+  return launch_kv_read_cache(p, cache, table, table_width, n_seqs, k, v, st, static_cast<cudaStream_t>(stream));
 }
 
 long long attn_fwd_varlen_workspace_bytes(int Tq, int n_seqs, int Hq, int Hkv, int d) {
@@ -655,7 +676,7 @@ long long attn_fwd_paged_workspace_bytes(const attn_kv_cache_t* cache, int Tq, i
   if (rc != ATTN_OK) return -1;
   if (cache->n_pages == 0) max_kv = 0;
   const PagedPlan pl = paged_plan(cache, Tq, n_seqs, max_q, Hq, max_kv);
-  return paged_space(pl, Tq, n_seqs, Hq, cache->d).all();
+  return paged_space(pl, Tq, n_seqs, Hq, cache->Hkv, cache->d).all();
 }
 
 int attn_fwd_paged(const void* q, const attn_kv_cache_t* cache, void* o, float* lse, int Tq, int n_seqs, int max_q,
@@ -676,7 +697,7 @@ int attn_fwd_paged(const void* q, const attn_kv_cache_t* cache, void* o, float* 
     return ATTN_ERR_MISALIGNED;
   if (cache->n_pages == 0) max_kv = 0;  // there is nothing to read
   const PagedPlan pl = paged_plan(cache, Tq, n_seqs, max_q, Hq, max_kv);
-  const PagedSpace sp = paged_space(pl, Tq, n_seqs, Hq, d);
+  const PagedSpace sp = paged_space(pl, Tq, n_seqs, Hq, cache->Hkv, d);
   if (sp.all() > 0) {
     if (workspace == nullptr || workspace_bytes < sp.all()) return ATTN_ERR_INVALID_ARG;
     if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
@@ -722,7 +743,23 @@ int attn_fwd_paged(const void* q, const attn_kv_cache_t* cache, void* o, float* 
     c.o_part = o_part;
     c.lse_part = lse_part;
     c.plan = static_cast<int*>(workspace);
-    rc = cache->dtype == ATTN_FP8_E4M3 ? launch_ragged_d<3>(c, st, s) : launch_ragged_d<2>(c, st, s);
+    if (pl.expand > 0) {
+      char* kv = ws + sp.head + sp.o + sp.lse;
+      KvReadParams rp = {};
+      rp.lens = kv_lens;
+      rp.stride = pl.expand;
+      rp.T = (long long)n_seqs * pl.expand;
+      if ((rc = launch_kv_read_cache(rp, cache, table, table_width, n_seqs, kv, kv + sp.kv, st, s)) != ATTN_OK) return rc;
+      c.k = kv;
+      c.v = kv + sp.kv;
+      c.k_stride = c.v_stride = (long long)cache->Hkv * d;
+      c.Tk = n_seqs * pl.expand;
+      c.seq_stride = pl.expand;
+      c.cache = nullptr;
+      rc = launch_ragged_d<1>(c, st, s);
+    } else {
+      rc = cache->dtype == ATTN_FP8_E4M3 ? launch_ragged_d<3>(c, st, s) : launch_ragged_d<2>(c, st, s);
+    }
     if (rc != ATTN_OK || pl.n_windows == 1) return rc;
     WindowParams wp;
     static_cast<PagedSeqs&>(wp) = seqs;
