@@ -6,15 +6,15 @@
 #include <cstdint>
 
 #include "ptx.cuh"
+#include "ragged_pick.cuh"
 
 namespace attn {
 
-// Packed sequences (one-block-per-item kernel, RAGGED configurations): the
-// work items come from a list in device memory (ragged_plan_kernel).
+// Packed sequences (one-block-per-item kernel, RAGGED configurations): each
+// block picks its work item, or takes it from a list in device memory, items of 8
+// ints: seq (-1: none), block, q0, nq, k0, nk, 0, 0.
 struct RaggedParams {
-  const int* plan;   // items of 8 ints: seq (-1: none), block, q0, nq, k0, nk, 0, 0
-  int max_items;     // items that the launch's grid has room for
-  int Tq;            // query tokens in all (lse rows)
+  PlanParams seqs;   // max_items: items that the launch's grid has room for
   const int* table;  // paged: page table [n_seqs, table_width]
   int table_width, page_shift, n_pages;
   const unsigned char *k_exp, *v_exp;  // e4m3 cache: exponent bytes [n_pages, page_size, Hkv]
@@ -196,11 +196,14 @@ struct FwdCfg {
   // register split (two softmax warpgroups: 384 threads launch with 168
   // registers each = 64512; the softmax warpgroups get 200, the control
   // warpgroup 104: 2*128*200 + 128*104 = 64512)
-  static constexpr int REG_LAUNCH = 65536 / NTHREADS >= 255 ? 255 : (65536 / NTHREADS) / 8 * 8;
-  static constexpr bool SPLIT_REGS = NQT * NS == 2;
+  // (two blocks of one query tile sharing an SM, packed sequences at d = 64: 256
+  // threads launch with 128; 128*200 + 128*56 = 32768)
+  static constexpr int BPS = RAGGED != 0 && D == 64 && NQT == 1 ? 2 : 1;
+  static constexpr int REG_LAUNCH = 65536 / BPS / NTHREADS >= 255 ? 255 : (65536 / BPS / NTHREADS) / 8 * 8;
+  static constexpr bool SPLIT_REGS = NQT * NS == 2 || BPS == 2;
   // (KV8: 512 threads launch with 128; 2*128*200 + 2*128*56 = 65536)
-  static constexpr int REG_SOFTMAX = 200, REG_CONTROL = KV8 ? 56 : 104;
-  static_assert(!SPLIT_REGS || 2 * 128 * REG_SOFTMAX + (NTHREADS - 256) * REG_CONTROL <= NTHREADS * REG_LAUNCH,
+  static constexpr int REG_SOFTMAX = 200, REG_CONTROL = KV8 || BPS == 2 ? 56 : 104;
+  static_assert(!SPLIT_REGS || 32 * SM_WARPS * REG_SOFTMAX + (NTHREADS - 32 * SM_WARPS) * REG_CONTROL <= NTHREADS * REG_LAUNCH,
                 "register split exceeds the launch allocation");
   static constexpr uint32_t IDESC_QK = ptx::idesc<FP8>(128, BN, false);
   static constexpr uint32_t IDESC_PV = ptx::idesc<FP8>(128, D, true);

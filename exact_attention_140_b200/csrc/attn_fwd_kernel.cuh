@@ -64,7 +64,7 @@ namespace attn {
 
 
 template <class Cfg>
-__global__ void __launch_bounds__(Cfg::NTHREADS, 1)
+__global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
   constexpr int BM = Cfg::BM, BN = Cfg::BN, D = Cfg::D, NQT = Cfg::NQT, SB = Cfg::SB;
@@ -86,15 +86,38 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
   if constexpr (Cfg::RAGGED != 0) {
     // bands of heads as below, the listed items (longest first) within a band
     ptx::grid_dep_launch();
-    ptx::grid_dep_wait();
     split = (int)blockIdx.x % p.n_splits;
-    const int L = (int)blockIdx.x / p.n_splits, per = p.band * p.rg.max_items;
+    const int L = (int)blockIdx.x / p.n_splits, per = p.band * p.rg.seqs.max_items;
     const int bi = L / per, within = L - bi * per;
     const int bsz = p.nh - bi * p.band < p.band ? p.nh - bi * p.band : p.band;
     const int item = within / bsz;
-    // (from L2: the list was written while this grid was being launched)
-    const int4 i0 = __ldcg(reinterpret_cast<const int4*>(p.rg.plan) + 2 * item);
-    const int2 i1 = __ldcg(reinterpret_cast<const int2*>(p.rg.plan) + 2 + 4 * item);
+    int4 i0;
+    int2 i1;
+    if (p.rg.seqs.plan == nullptr) {
+      int* s_item = reinterpret_cast<int*>(sgen);  // (nothing has been loaded yet)
+      if (warp == 0) {
+        const bool there = ragged_pick(p.rg.seqs, item, i0, i1);
+        if (lane == 0) {
+          s_item[0] = there ? i0.x : -1;
+          if (there) {
+            s_item[1] = i0.y;
+            s_item[2] = i0.z;
+            s_item[3] = i0.w;
+            s_item[4] = i1.x;
+            s_item[5] = i1.y;
+          }
+        }
+      }
+      __syncthreads();
+      // (all have read it before the first load lands there: the barrier below comes between)
+      i0 = make_int4(s_item[0], s_item[1], s_item[2], s_item[3]);
+      i1 = make_int2(s_item[4], s_item[5]);
+    } else {
+      ptx::grid_dep_wait();
+      // (from L2: the list was written while this grid was being launched)
+      i0 = __ldcg(reinterpret_cast<const int4*>(p.rg.seqs.plan) + 2 * item);
+      i1 = __ldcg(reinterpret_cast<const int2*>(p.rg.seqs.plan) + 2 + 4 * item);
+    }
     if (i0.x < 0) return;
     hy = bi * p.band + within % bsz;
     b = 0;
@@ -384,7 +407,7 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
       bool final_out;
       if constexpr (Cfg::RAGGED != 0) {
         tok = (long long)q_base + row;
-        lse_at = (long long)h * p.rg.Tq + tok;
+        lse_at = (long long)h * p.rg.seqs.Tq + tok;
         final_out = p.o_part == nullptr || nk_all <= p.kv_chunk;  // (one window only)
       } else {
         tok = (long long)b * p.Nq + row;
@@ -416,7 +439,7 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, 1)
         // split-KV partial of window `split`: fp32 O_s and LSE_s
         long long prow, plse;
         if constexpr (Cfg::RAGGED != 0) {
-          prow = plse = ((long long)split * p.rg.Tq + tok) * p.Hq + h;
+          prow = plse = ((long long)split * p.rg.seqs.Tq + tok) * p.Hq + h;
         } else {
           const long long zs = (long long)split * p.B + b;
           prow = (zs * p.Nq + row) * p.Hq + h;

@@ -1,11 +1,16 @@
-// ragged_plan.cuh -- the list of work items of an attention over packed
-// sequences: one item per (sequence, block of query rows), longest first.
+// ragged_plan.cuh -- the work items of an attention over packed sequences: one
+// item per (sequence, block of query rows), longest first.
 //
-// The lengths live on the device, so the host cannot build the list; one block
-// does, ahead of the attention kernel (whose launch overlaps it).  An item's
-// cost is the number of key tiles its last row sees; items are handed out in
-// falling order of cost by a counting sort over kPlanBuckets levels (the order
-// within a level is arbitrary and does not affect any result).
+// The lengths live on the device, so the host cannot list the items.  An item's
+// cost is the number of key tiles its last row sees.  One block lists them ahead of
+// the attention kernel (whose launch overlaps it) by a counting sort over
+// kPlanBuckets levels of cost (the order within a level is arbitrary and does not
+// affect any result); that kernel takes 5 us.  In a small call every block of the
+// attention kernel finds its own item instead (ragged_pick): within a sequence the
+// cost grows with the block, so the number of items that cost at least c has a
+// closed form for each sequence, and a bisection over c with a warp's sum over the
+// sequences finds the item of a given rank.  That takes every block about 1 us,
+// so a call of more blocks than SMs has the list.
 #pragma once
 #include <cstdint>
 
@@ -17,32 +22,6 @@ namespace attn {
 
 constexpr int kPlanThreads = 512;
 constexpr int kPlanBuckets = 256;
-constexpr int kPlanItem = 8;   // ints of an item
-
-struct PlanParams {
-  int* plan;
-  int max_items;
-  int n_seqs, Tq, Tk, max_q, max_kv;
-  const int* cu_q;     // or nullptr: sequence s has the rows [s * max_q, (s + 1) * max_q)
-  const int* cu_k;     // packed keys; nullptr: paged
-  const int* kv_lens;  // paged, or (k_stride > 0) packed with sequence s at k_stride * s
-  int k_stride;
-  int rows_per_token;  // packed rows of a token (1 or the group size)
-  int block_rows, bn;
-  bool causal;
-  unsigned int* err;
-};
-
-// A boundary pair of the device clamped to [0, total].
-__device__ __forceinline__ int2 clamped_range(const int* cu, int s, int total, bool& bad) {
-  int a = __ldg(cu + s), b = __ldg(cu + s + 1);
-  if (a < 0 || b < a || b > total) {
-    bad = true;
-    a = a < 0 ? 0 : (a > total ? total : a);
-    b = b < a ? a : (b > total ? total : b);
-  }
-  return make_int2(a, b);
-}
 
 __global__ void __launch_bounds__(kPlanThreads) ragged_plan_kernel(const PlanParams p) {
   __shared__ int s_hist[kPlanBuckets], s_max, s_count;
@@ -54,34 +33,13 @@ __global__ void __launch_bounds__(kPlanThreads) ragged_plan_kernel(const PlanPar
   __syncthreads();
   bool bad = false;
   auto seq = [&](int s, int& q0, int& nq, int& k0, int& nk) {
-    if (p.cu_q != nullptr) {
-      const int2 q = clamped_range(p.cu_q, s, p.Tq, bad);
-      q0 = q.x;
-      nq = q.y - q.x;
-    } else {
-      q0 = s * p.max_q;
-      nq = p.max_q;
-    }
-    if (nq > p.max_q) {
-      bad = true;
-      nq = p.max_q;
-    }
-    if (p.cu_k != nullptr) {
-      const int2 k = clamped_range(p.cu_k, s, p.Tk, bad);
-      k0 = k.x;
-      nk = k.y - k.x;
-    } else {
-      k0 = s * p.k_stride;
-      nk = __ldg(p.kv_lens + s);
-      if (nk < 0 || nk > p.max_kv) {
-        bad = true;
-        nk = nk < 0 ? 0 : p.max_kv;
-      }
-    }
+    const RaggedSeq r = ragged_seq(p, s, bad);
+    q0 = r.q0;
+    nq = r.nq;
+    k0 = r.k0;
+    nk = r.nk;
   };
-  auto blocks_of = [&](int nq) -> int {
-    return (int)(((long long)nq * p.rows_per_token + p.block_rows - 1) / p.block_rows);
-  };
+  auto blocks_of = [&](int nq) -> int { return ragged_blocks(p, nq); };
   auto cost = [&](int qb, int nq, int nk) -> int {  // key tiles of the block's last row
     const int last = (int)((((long long)(qb + 1) * p.block_rows) + p.rows_per_token - 1) / p.rows_per_token);
     return (int)((vis_end((last < nq ? last : nq) - 1, nq, nk, p.causal) + p.bn - 1) / p.bn);

@@ -142,10 +142,10 @@ struct PagedPlan {
   long long items;
   int window, n_windows, expand;
 };
-long long ragged_max_items(long long Tq, long long n_seqs, int Hq, int Hkv, int d);
-int ragged_block_rows(int d);
+long long ragged_max_items(long long Tq, long long n_seqs, int Hq, int Hkv, int block_rows);
+int ragged_block_rows(int d, bool prompts);
 int ragged_rows_per_token(int Hq, int Hkv);
-long long ragged_plan_bytes(long long items);
+long long ragged_plan_bytes(long long n_seqs, long long items, int nh);
 
 constexpr int kSms = 148;  // SMs of a B200: the grids and their workspace go by it
 // Rows of a block: one tile of 8 rows a warp, then two where the accumulators fit
@@ -180,12 +180,12 @@ PagedPlan paged_plan(const attn_kv_cache_t* c, int Tq, int n_seqs, int max_q, in
   const int Hkv = c->Hkv;
   const long long rows = (long long)max_q * (Hq / Hkv);
   if (rows > 64 && c->n_pages > 0) {
-    pl.items = ragged_max_items(Tq, n_seqs, Hq, Hkv, c->d);
+    pl.items = ragged_max_items(Tq, n_seqs, Hq, Hkv, ragged_block_rows(c->d, false));
     const int g = ragged_rows_per_token(Hq, Hkv);
     // Windows by an estimate in key times (one block, 256 rows, about 16 ns a key):
     // the waves of blocks times a window's keys and a block's fixed cost, and
     // writing and merging the partial rows (about 4 TB/s, 5 us to begin with).
-    const long long blocks = ((long long)Tq * g / ragged_block_rows(c->d) + (n_seqs + 1) / 2) * (g > 1 ? Hkv : Hq);
+    const long long blocks = ((long long)Tq * g / ragged_block_rows(c->d, false) + (n_seqs + 1) / 2) * (g > 1 ? Hkv : Hq);
     long long want = 1;
     double best = 0.0;
     for (long long n = 1; n <= 16 && (n == 1 || max_kv / n >= 512); ++n) {
@@ -239,7 +239,7 @@ PagedSpace paged_space(const PagedPlan& pl, long long Tq, long long n_seqs, long
   auto round = [](long long b) { return (b + 255) / 256 * 256; };
   PagedSpace s = {};
   if (pl.items > 0) {
-    s.head = ragged_plan_bytes(pl.items);
+    s.head = ragged_plan_bytes(n_seqs, pl.items, (int)(ragged_rows_per_token((int)Hq, (int)Hkv) > 1 ? Hkv : Hq));
     if (pl.n_windows > 1) {
       s.o = round(pl.n_windows * Tq * Hq * d * 4);
       s.lse = round(pl.n_windows * Tq * Hq * 4);
@@ -334,18 +334,29 @@ int launch_paged(const PagedParams& p, const PagedPlan& pl, const attn_kv_cache_
 // The heads of a group are always stacked where the group divides the tile: a
 // block then covers fewer tokens, which wastes less of a causal block's diagonal
 // and of a short sequence, and a key tile is read once per group.
-template <bool C, int R> using CfgRagD64 = FwdCfg<64, 128, 2, 3, 3, C, false, 0, 1, false, 1, true, false, R>;
+// Causal packed prompts at d = 64: blocks of one query tile, two sharing an SM,
+// whose starts and ends overlap each other's work (prompts up to 1024, 12 heads: 32.5
+// -> 29.9 us, up to 4096: 115 -> 107; not causal 167 -> 169, over a cache 136 -> 140).
+template <bool C, int R> using CfgRagD64 = std::conditional_t<C && R == 1, FwdCfg<64, 128, 1, 2, 2, C, false, 0, 1, false, 1, true, false, R>,
+                                                              FwdCfg<64, 128, 2, 3, 3, C, false, 0, 1, false, 1, true, false, R>>;
 template <bool C, int R> using CfgRagD128 = FwdCfg<128, 128, 2, 2, 2, C, false, 0, 1, false, 1, true, false, R>;
 template <bool C, int R> using CfgRagD256 = FwdCfg<256, 64, 1, 2, 2, C, false, 0, 2, false, 1, true, false, R>;
 
-int ragged_block_rows(int d) { return d == 256 ? 128 : 256; }
+// Rows of a block (packed prompts: at least).
+int ragged_block_rows(int d, bool prompts) { return d == 256 || (d == 64 && prompts) ? 128 : 256; }
 int ragged_rows_per_token(int Hq, int Hkv) { return pack_factor(Hq, Hkv); }
 // Items at most: every sequence may end in a block of one row.
-long long ragged_max_items(long long Tq, long long n_seqs, int Hq, int Hkv, int d) {
-  const long long R = ragged_block_rows(d), n = n_seqs < Tq ? n_seqs : Tq;
-  return (Tq * ragged_rows_per_token(Hq, Hkv) + n * (R - 1)) / R;
+long long ragged_max_items(long long Tq, long long n_seqs, int Hq, int Hkv, int block_rows) {
+  const long long n = n_seqs < Tq ? n_seqs : Tq;
+  return (Tq * ragged_rows_per_token(Hq, Hkv) + n * (block_rows - 1)) / block_rows;
 }
-long long ragged_plan_bytes(long long items) { return (4 * kPlanItem * items + 255) / 256 * 256; }
+// Whether the items are listed ahead: with many sequences, or where an SM has more
+// than one block to start (finding its item takes a block about 1 us, the list 5 us
+// and a launch: 4 prompts of up to 100 tokens 26 -> 18 us a call without it).
+bool ragged_listed(long long n_seqs, long long items, int nh) { return n_seqs > kPickSeqs || items * nh > kSms; }
+long long ragged_plan_bytes(long long n_seqs, long long items, int nh) {
+  return ragged_listed(n_seqs, items, nh) ? (4 * kPlanItem * items + 255) / 256 * 256 : 0;
+}
 
 struct RaggedCall {
   const void *q, *k, *v;
@@ -370,7 +381,7 @@ int launch_ragged(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
   int rc = set_smem_once(attn_fwd_kernel<Cfg>, (int)Cfg::SMEM_BYTES, attr_set, st);
   if (rc != ATTN_OK) return rc;
   const int g = ragged_rows_per_token(c.Hq, c.Hkv);
-  const long long items = ragged_max_items(c.Tq, c.n_seqs, c.Hq, c.Hkv, c.d);
+  const long long items = ragged_max_items(c.Tq, c.n_seqs, c.Hq, c.Hkv, Cfg::BM * Cfg::NQT);
   const int nh = g > 1 ? c.Hkv : c.Hq;
   const long long blocks = items * nh * c.n_windows;
   if (blocks > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;
@@ -395,7 +406,7 @@ int launch_ragged(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
       return ATTN_ERR_CUDA;
   }
   PlanParams pp;
-  pp.plan = c.plan;
+  pp.plan = ragged_listed(c.n_seqs, items, nh) ? c.plan : nullptr;
   pp.max_items = (int)items;
   pp.n_seqs = c.n_seqs;
   pp.Tq = c.Tq;
@@ -411,9 +422,11 @@ int launch_ragged(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
   pp.bn = Cfg::BN;
   pp.causal = c.causal;
   pp.err = st->err;
-  ATTN_LOGF("attn: ragged_plan_kernel grid=(1) block=%d seqs=%d items<=%lld\n", kPlanThreads, c.n_seqs, items);
-  ragged_plan_kernel<<<1, kPlanThreads, 0, s>>>(pp);
-  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  if (pp.plan != nullptr) {
+    ATTN_LOGF("attn: ragged_plan_kernel grid=(1) block=%d seqs=%d items<=%lld\n", kPlanThreads, c.n_seqs, items);
+    ragged_plan_kernel<<<1, kPlanThreads, 0, s>>>(pp);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  }
 
   FwdParams p = {};
   p.o = c.o;
@@ -438,9 +451,7 @@ int launch_ragged(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
   const long long kv_head = 4ll * c.Tk * c.d / (g > 1 ? 1 : p.group);
   long long band = (48ll << 20) / (kv_head > 0 ? kv_head : 1);
   p.band = (int)(band < 1 ? 1 : (band > nh ? nh : band));
-  p.rg.plan = c.plan;
-  p.rg.max_items = (int)items;
-  p.rg.Tq = c.Tq;
+  p.rg.seqs = pp;
   p.rg.table = c.table;
   p.rg.table_width = c.table_width;
   p.rg.page_shift = c.cache != nullptr ? page_shift(c.cache) : 0;
@@ -454,7 +465,11 @@ int launch_ragged(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
                   Cfg::RAGGED == 1 ? "" : (Cfg::KV8 ? " (paged e4m3)" : " (paged)"), c.n_windows, c.window, g, p.band);
     log_launch<Cfg>("attn_fwd_kernel", grid, c.n_seqs, c.Hq, c.Hkv, c.Tq, c.Tk, extra);
   }
-  // (the launch overlaps the plan kernel, which the kernel waits for)
+  if (pp.plan == nullptr) {
+    attn_fwd_kernel<Cfg><<<grid, Cfg::NTHREADS, Cfg::SMEM_BYTES, s>>>(tq, tk, tv, p);
+    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  }
+  // (the launch overlaps the list's kernel, which the attention kernel waits for)
   return launch_dependent(attn_fwd_kernel<Cfg>, blocks, Cfg::NTHREADS, Cfg::SMEM_BYTES, s, tq, tk, tv, (const FwdParams)p);
 }
 template <int R>
@@ -618,7 +633,8 @@ int attn_kv_read(const attn_kv_cache_t* cache, const int* table, int table_width
 long long attn_fwd_varlen_workspace_bytes(int Tq, int n_seqs, int Hq, int Hkv, int d) {
   if (Tq < 0 || n_seqs < 0 || Hq < 0 || Hkv < 1 || Hq % Hkv != 0 || !head_size_ok(d)) return -1;
   if (Tq == 0 || n_seqs == 0 || Hq == 0) return 0;
-  return ragged_plan_bytes(ragged_max_items(Tq, n_seqs, Hq, Hkv, d));
+  return ragged_plan_bytes(n_seqs, ragged_max_items(Tq, n_seqs, Hq, Hkv, ragged_block_rows(d, true)),
+                           ragged_rows_per_token(Hq, Hkv) > 1 ? Hkv : Hq);
 }
 
 int attn_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse, int Tq, int Tk, int n_seqs,
@@ -638,9 +654,11 @@ int attn_fwd_varlen(const void* q, const void* k, const void* v, void* o, float*
   if (!aligned16(o) || ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(cu_q) |
                          reinterpret_cast<uintptr_t>(cu_k)) & 3u) != 0)
     return ATTN_ERR_MISALIGNED;
-  if (workspace == nullptr || workspace_bytes < attn_fwd_varlen_workspace_bytes(Tq, n_seqs, Hq, Hkv, d))
-    return ATTN_ERR_INVALID_ARG;
-  if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
+  const long long need = attn_fwd_varlen_workspace_bytes(Tq, n_seqs, Hq, Hkv, d);
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
+  }
   int dev = 0;
   DeviceState* st = nullptr;
   if ((rc = device_state(&dev, &st)) != ATTN_OK) return rc;

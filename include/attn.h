@@ -483,8 +483,9 @@ int attn_kv_read(const attn_kv_cache_t *cache, const int *table, int table_width
  *              same array); read on the device only, so a call can be captured
  *              in a graph and replayed with other lengths
  *   workspace  DEVICE scratch, 16-byte aligned, of at least
- *              attn_fwd_varlen_workspace_bytes(Tq, n_seqs, Hq, Hkv, d) bytes, owned by
- *              the caller; calls that may overlap on the GPU need their own
+ *              attn_fwd_varlen_workspace_bytes(Tq, n_seqs, Hq, Hkv, d) bytes (0 in a
+ *              small call: workspace may be NULL), owned by the caller; calls
+ *              that may overlap on the GPU need their own
  * What one sequence holds never reaches another's rows, not even NaN.  Within a
  * sequence keys and values must be finite where a causal mask hides them (a
  * hidden NaN or infinity may reach rows of the same 128-row tile).
@@ -514,6 +515,8 @@ int attn_fwd_varlen(const void *q, const void *k, const void *v, void *o, float 
  * How a sequence's keys are shared out between blocks depends on the other
  * sequences of the call, and with it the last bits of the result.
  * The cache's memory behind a sequence's last token may hold anything, NaN too.
+ * As in attn_fwd_varlen, a cached key or value that the causal mask hides from a
+ * row of a chunk must be finite: it may reach the rows of its tile.
  */
 long long attn_fwd_paged_workspace_bytes(const attn_kv_cache_t *cache, int Tq, int n_seqs, int max_q, int Hq,
                                          int max_kv);

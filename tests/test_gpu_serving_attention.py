@@ -283,49 +283,65 @@ def test_prompt_then_steps(e4m3):
         assert torch.equal(rk, k)
 
 
-def test_graph_replayed_with_other_lengths():
-    """Lengths, boundaries and pages are read on the device: one captured step serves later ones."""
+@pytest.mark.parametrize("many", [1, 30])
+def test_graph_replayed_with_other_lengths(many):
+    """Lengths, boundaries and pages are read on the device: one captured step serves later ones (small calls, and
+    calls whose work is listed, shared between blocks and merged by further kernels)."""
     torch, ea, su = setup()
     Hq, Hkv, d = 8, 2, 128
-    cache, table, ks, vs = su.make_cache(ea, [300, 300, 300], 16, Hkv, d, True, seed=1)
-    lens, cu = su.i32(300, 300, 300), su.i32(0, 1, 2, 3)
-    q = rand(torch, 3, Hq, d, seed=1)
-    cq = su.i32(0, 100, 260)
-    x = rand(torch, 260, 4, 64, seed=2)
+    n = 5 * many
+    cache, table, ks, vs = su.make_cache(ea, [300] * n, 16, Hkv, d, True, seed=1)
+    lens, cu = su.i32(*[300] * n), su.starts([1] * n)
+    q = rand(torch, n, Hq, d, seed=1)
+    cq = su.starts([60] * n)
+    T = 60 * n
+    x = rand(torch, T, 4, 64, seed=2)
+    chunk = rand(torch, 4 * n, 24, 128, seed=3)  # 48 rows of 12 heads each and more than 64 in all of one
+    cc = su.starts([4] * n)
+
+    def step():
+        return (ea.attention_paged(q, cache, table, lens, cu_q=cu, max_q=1),
+                ea.attention_varlen(x[:, :2], x[:, 2:3], x[:, 3:], cq, cq, causal=True),
+                ea.attention_paged(chunk, cache, table, lens, cu_q=cc, max_q=8))
+
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
         for _ in range(2):
-            ea.attention_paged(q, cache, table, lens, cu_q=cu, max_q=1)
-            ea.attention_varlen(x[:, :2], x[:, 2:3], x[:, 3:], cq, cq, causal=True)
+            step()
     torch.cuda.current_stream().wait_stream(side)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        o, lse = ea.attention_paged(q, cache, table, lens, cu_q=cu, max_q=1)
-        o2, l2 = ea.attention_varlen(x[:, :2], x[:, 2:3], x[:, 3:], cq, cq, causal=True)
-    for new, c in (([300, 300, 300], [0, 100, 260]), ([7, 160, 299], [0, 259, 260]), ([1, 0, 64], [0, 30, 200])):
+        (o, lse), (o2, l2), (o3, l3) = step()
+    for new, c in (([300] * 5, [0, 100, 260, 260, 280, 300]), ([7, 160, 299, 8, 50], [0, 259, 260, 261, 262, 263]),
+                   ([1, 0, 64, 300, 128], [0, 30, 200, 201, 250, 251])):
+        new, c = new * many, [i + 300 * m for m in range(many) for i in c[:-1]] + [300 * (many - 1) + c[-1]]
         lens.copy_(su.i32(*new))
         cq.copy_(su.i32(*c))
         graph.replay()
         su.no_device_error(ea)
-        for i, n in enumerate(new):
-            su.check_attention(o[i:i + 1], lse[:, i:i + 1],
-                               su.attention(q[i:i + 1], ks[i][:n], vs[i][:n], True, 1 / math.sqrt(d)), d)
-        for s in (slice(c[0], c[1]), slice(c[1], c[2])):
-            su.check_attention(o2[s], l2[:, s], su.attention(x[s, :2], x[s, 2:3], x[s, 3:], True, 0.125), 64)
+        for i in range(0, n, 1 if many == 1 else 7):
+            m, scale = new[i], 1 / math.sqrt(d)
+            su.check_attention(o[i:i + 1], lse[:, i:i + 1], su.attention(q[i:i + 1], ks[i][:m], vs[i][:m], True, scale), d)
+            s = slice(4 * i, 4 * i + 4)
+            su.check_attention(o3[s], l3[:, s], su.attention(chunk[s], ks[i][:m], vs[i][:m], True, scale), d)
+            s = slice(c[i], c[i + 1])
+            if s.stop > s.start:
+                su.check_attention(o2[s], l2[:, s], su.attention(x[s, :2], x[s, 2:3], x[s, 3:], True, 0.125), 64)
 
 
-def test_calls_on_two_streams():
+@pytest.mark.parametrize("n", [3, 60, 150])
+def test_calls_on_two_streams(n):
     """Calls with workspaces of their own may overlap."""
     torch, ea, su = setup()
-    lens = [900, 1200, 40]
-    cache, table, ks, vs = su.make_cache(ea, lens, 16, 2, 128, False, seed=4)
-    q = rand(torch, 3, 8, 128, seed=5)
-    want = ea.attention_paged(q, cache, table, su.i32(*lens))
-    x = rand(torch, 500, 6, 128, seed=6)
-    cu = su.i32(0, 130, 500)
-    want2 = ea.attention_varlen(x[:, :4], x[:, 4:5], x[:, 5:], cu, cu, causal=True)
+    lens = ([900, 1200, 40] * n)[:n]
+    cache, table, ks, vs = su.make_cache(ea, lens, 16, 2, 128, n != 60, seed=4)
+    q = rand(torch, n, 8, 128, seed=5)
     kv = su.i32(*lens)
+    want = ea.attention_paged(q, cache, table, kv)
+    x = rand(torch, 50 * n, 6, 128, seed=6)
+    cu = su.starts([50] * n)
+    want2 = ea.attention_varlen(x[:, :4], x[:, 4:5], x[:, 5:], cu, cu, causal=True)
     torch.cuda.synchronize()
     s = [torch.cuda.Stream() for _ in range(2)]
     got = []
@@ -337,3 +353,141 @@ def test_calls_on_two_streams():
     for i in range(0, 24, 2):
         assert all(torch.equal(a, b) for a, b in zip(got[i], want))
         assert all(torch.equal(a, b) for a, b in zip(got[i + 1], want2))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("lens", [[1] * 3, [64, 128, 129, 1], [3000] * 40 + [5] * 60, [0, 0, 7], [33000, 12], [500] * 300])
+def test_decoding_lengths(lens, e4m3):
+    """One token of every sequence: lengths at the borders of units, one long sequence shared by all blocks, many
+    short ones in a block's run, and sequences without a key."""
+    torch, ea, su = setup()
+    cache, table, ks, vs = su.make_cache(ea, lens, 32, 2, 64, e4m3, seed=len(lens))
+    n = len(lens)
+    q = rand(torch, n, 12, 64, seed=7)
+    o, lse = ea.attention_paged(q, cache, table, su.i32(*lens))
+    su.no_device_error(ea)
+    for i in range(0, n, 1 if n < 10 else 11):
+        su.check_attention(o[i:i + 1], lse[:, i:i + 1], su.attention(q[i:i + 1], ks[i], vs[i], True, 0.125), 64)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("scale", [0.0, -0.08, 0.6])
+@pytest.mark.parametrize("n", [1, 3, 90])
+def test_paged_scales(n, scale, e4m3):
+    torch, ea, su = setup()
+    cache, table, ks, vs = su.make_cache(ea, [400], 64, 2, 128, e4m3, seed=6)
+    q = rand(torch, n, 8, 128, seed=n)
+    o, lse = ea.attention_paged(q, cache, table, su.i32(400), scale=scale)
+    su.check_attention(o, lse, su.attention(q, ks[0], vs[0], True, scale), 128)
+
+
+def test_scales_of_far_apart_powers():
+    """Rows of an e4m3 cache whose scales differ by 2^60 and more, large values on keys of no weight among them."""
+    torch, ea, su = setup()
+    cache, table, ks, vs = su.make_cache(ea, [500], 16, 1, 128, True, seed=6)
+    k_exp, v_exp = cache.tensors[2], cache.tensors[3]
+    ids = table[0].long()
+    i = torch.arange(500, device="cuda")
+    e = torch.where(i % 3 == 0, 60, torch.where(i % 3 == 1, 120, 150)).to(torch.uint8)  # 2^-67, 2^-7, 2^23
+    v_exp[ids[i // 16], i % 16, 0] = e
+    v = cache.tensors[1][ids[i // 16], i % 16].view(torch.float8_e4m3fn).double() * su.pow2(e.long() - 127)[:, None, None]
+    for n in (1, 100):
+        q = rand(torch, n, 4, 128, seed=n)
+        # the keys with the large values all but hidden: their scores far below the others'
+        k2 = ks[0].clone()
+        o, lse = ea.attention_paged(q, cache, table, su.i32(500))
+        su.check_attention(o, lse, su.attention(q, k2, v, True, 1 / math.sqrt(128)), 128)
+
+
+def test_queries_of_far_apart_sizes():
+    """f16 products over an e4m3 cache: query rows from 1e-30 to 1e30, and elements of one row that differ by 2^30."""
+    torch, ea, su = setup()
+    cache, table, ks, vs = su.make_cache(ea, [300] * 4, 16, 1, 128, True, seed=8)
+    q = rand(torch, 4, 4, 128, seed=3).float()
+    q[0] *= 1e-30
+    q[1] *= 1e-3
+    q[1, :, ::2] *= 2.0 ** -30
+    q[2, 0] = 0
+    q = q.to(torch.bfloat16)
+    o, lse = ea.attention_paged(q, cache, table, su.i32(300, 300, 300, 300))
+    for i in range(4):
+        su.check_attention(o[i:i + 1], lse[:, i:i + 1],
+                           su.attention(q[i:i + 1], ks[i], vs[i], True, 1 / math.sqrt(128)), 128)
+    big = (rand(torch, 1, 4, 128, seed=3).float() * 1e30).to(torch.bfloat16)
+    o, _ = ea.attention_paged(big, cache, table[:1], su.i32(300), scale=1e-31)
+    su.check_attention(o, None, su.attention(big, ks[0], vs[0], True, 1e-31), 128)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_cache_beyond_32_bits(e4m3):
+    """Pages whose elements lie past 2^31 and 2^32: write, read and both attention kernels."""
+    torch, ea, su = setup()
+    page, Hkv, d = 16, 8, 128
+    n_pages = (1 << 32) // (page * Hkv * d) + 40
+    shape = (n_pages, page, Hkv, d)
+    t = [torch.empty(shape, dtype=torch.uint8 if e4m3 else torch.bfloat16, device="cuda") for _ in range(2)]
+    e = [torch.empty(shape[:3], dtype=torch.uint8, device="cuda") for _ in range(2)] if e4m3 else []
+    cache = ea.KVCache(*t, *e)
+    T = 200
+    kv = rand(torch, T, 2 * Hkv, d, seed=1)
+    pages = torch.tensor([n_pages - 1 - 2 * i for i in range(10)] + [n_pages // 2 + i for i in range(3)], device="cuda")
+    table = pages.to(torch.int32).view(1, -1)
+    i = torch.arange(T, device="cuda")
+    ea.kv_write(cache, kv[:, :Hkv], kv[:, Hkv:], pages[i // page] * page + i % page)
+    k, v = ea.kv_read(cache, table, su.i32(0, T), T)
+    su.no_device_error(ea)
+    if e4m3:
+        val, ex = su.quantise(kv)
+        want = val * su.pow2(ex - 127).unsqueeze(-1)
+    else:
+        want = kv.double()
+    assert torch.equal(k.double(), want[:, :Hkv]) and torch.equal(v.double(), want[:, Hkv:])
+    for n in (1, 40, 150):
+        q = rand(torch, n, 16, d, seed=n)
+        o, lse = ea.attention_paged(q, cache, table, su.i32(T))
+        su.check_attention(o, lse, su.attention(q, k, v, True, 1 / math.sqrt(d)), d)
+    del t, e, cache
+    torch.cuda.empty_cache()
+
+
+def test_empty_calls():
+    torch, ea, su = setup()
+    z = torch.empty(0, 4, 128, dtype=torch.bfloat16, device="cuda")
+    o, lse = ea.attention_varlen(z, z, z, su.i32(0), su.i32(0), causal=True)
+    assert o.shape == (0, 4, 128) and lse.shape == (4, 0)
+    q = rand(torch, 5, 4, 128, seed=1)
+    o, lse = ea.attention_varlen(q, z, z, su.i32(0, 5), su.i32(0, 0), causal=False)  # queries, but no key anywhere
+    assert bool((o == 0).all()) and bool((lse == -math.inf).all())
+    none = torch.empty(0, 16, 4, 128, dtype=torch.bfloat16, device="cuda")
+    cache = ea.KVCache(none, none.clone())
+    for n in (5, 1):
+        o, lse = ea.attention_paged(q[:n], cache, torch.zeros(n, 3, dtype=torch.int32, device="cuda"),
+                                    torch.zeros(n, dtype=torch.int32, device="cuda"))
+        assert bool((o == 0).all()) and bool((lse == -math.inf).all())
+    q90 = rand(torch, 90, 4, 128, seed=1)
+    o, lse = ea.attention_paged(q90, cache, torch.zeros(1, 3, dtype=torch.int32, device="cuda"), su.i32(0))
+    assert bool((o == 0).all())
+    ea.kv_write(cache, z, z, torch.empty(0, dtype=torch.int64, device="cuda"))
+    k, _ = ea.kv_read(cache, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), su.i32(0, 0), 0)
+    assert k.shape == (0, 4, 128)
+    su.no_device_error(ea)
+
+
+def test_tensors_elsewhere_are_refused():
+    torch, ea, su = setup()
+    q = rand(torch, 5, 4, 64, seed=1)
+    with pytest.raises(ValueError):
+        ea.attention_varlen(q, q.cpu(), q.cpu(), su.i32(0, 5), su.i32(0, 5))
+    with pytest.raises(ValueError):
+        ea.attention_varlen(q, q, q, su.i32(0, 5).cpu(), su.i32(0, 5))
+    pages = torch.zeros(2, 16, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        ea.attention_paged(q, ea.KVCache(pages, pages.clone()), torch.zeros(5, 1, dtype=torch.int32, device="cuda"),
+                           torch.ones(5, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        ea.qk_norm_rope(q, q, torch.arange(5, device="cuda"),
+                        ea.Rope(freqs=ea.rope_freqs(64, 1e4, device="cpu")[0], rot_dim=64))
+    with pytest.raises(TypeError):
+        ea.attention_varlen(q.float(), q, q, su.i32(0, 5), su.i32(0, 5))
+    with pytest.raises(TypeError):
+        ea.attention_varlen(q, q, q, su.i32(0, 5).long(), su.i32(0, 5))

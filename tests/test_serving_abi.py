@@ -98,7 +98,8 @@ def varlen(**kw):
     (dict(Tq=-1), INVALID), (dict(Tk=-1), INVALID), (dict(n=-1), INVALID), (dict(Hq=3), INVALID), (dict(Hkv=0), INVALID),
     (dict(causal=2), INVALID), (dict(scale=math.nan), INVALID), (dict(d=80), UNSUPPORTED), (dict(Hq=65536 * 2), UNSUPPORTED),
     (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(o=None), INVALID), (dict(cq=None), INVALID),
-    (dict(ws=None), INVALID), (dict(wsb=16), INVALID), (dict(ws=P + 8), MISALIGNED), (dict(o=P + 8), MISALIGNED),
+    (dict(n=200, Tq=300, ws=None), INVALID), (dict(n=200, Tq=300, wsb=16), INVALID),
+    (dict(n=200, Tq=300, ws=P + 8), MISALIGNED), (dict(o=P + 8), MISALIGNED),
     (dict(lse=P + 2), MISALIGNED), (dict(cq=P + 1), MISALIGNED), (dict(qs=100), INVALID), (dict(ks=260), MISALIGNED),
     (dict(Tq=0), OK), (dict(n=0), OK), (dict(Hq=0), OK)])
 def test_varlen_refusals(kw, status):
@@ -109,10 +110,13 @@ def test_varlen_workspace():
     f = ea.attn_fwd_varlen_workspace_bytes
     assert f(-1, 1, 4, 2, 128) == f(8, 1, 3, 2, 128) == f(8, 1, 4, 0, 128) == f(8, 1, 4, 2, 96) == -1
     assert f(0, 1, 4, 2, 128) == f(8, 0, 4, 2, 128) == 0
-    # a list of 32-byte items: blocks of 256 rows, groups of 4 stacked
-    assert f(1000, 3, 32, 8, 128) == (32 * ((4000 + 3 * 255) // 256) + 255) // 256 * 256
-    assert f(1000, 3, 8, 8, 256) == (32 * ((1000 + 3 * 127) // 128) + 255) // 256 * 256
-    assert f(5, 100, 8, 8, 128) == f(5, 5, 8, 8, 128)  # at most a sequence per token
+    assert f(1000, 128, 32, 8, 128) == (32 * ((4000 + 128 * 255) // 256) + 255) // 256 * 256
+    assert f(1000, 2, 32, 8, 128) == 0  # at most a block per SM: each finds its own item
+    # otherwise a list of 32-byte items: blocks of 256 rows (128 at other head sizes), groups of 4 stacked
+    assert f(1000, 150, 32, 8, 128) == (32 * ((4000 + 150 * 255) // 256) + 255) // 256 * 256
+    assert f(1000, 150, 8, 8, 256) == (32 * ((1000 + 150 * 127) // 128) + 255) // 256 * 256
+    assert f(100000, 2, 8, 8, 128) == (32 * ((100000 + 2 * 255) // 256) + 255) // 256 * 256
+    assert f(200, 500, 8, 8, 128) == (32 * ((200 + 200 * 255) // 256) + 255) // 256 * 256  # a sequence per token
 
 
 def paged(c=None, **kw):
@@ -146,9 +150,8 @@ def test_paged_workspace():
     # of the 2 blocks that an SM holds where those are fewer
     assert f(c, 50, 50, 1, 32, 192) == 512 + 2 * 296 * 8 * 128 * 4 + 2 * 296 * 8 * 4
     assert f(c, 64, 64, 1, 32, 1 << 17) == f(c, 64, 64, 1, 32, 1 << 20)  # the grid is bounded by the GPU
-    # 300 tokens of 4 stacked heads: the item list; with long contexts windows join it
-    items = (300 * 4 + 255) // 256
-    assert f(c, 300, 1, 300, 32, 500) == (32 * items + 255) // 256 * 256
+    # 300 tokens of 4 stacked heads: with long contexts partial rows of several key windows
+    assert f(c, 300, 1, 300, 32, 500) == 0
     assert f(c, 300, 1, 300, 32, 1 << 16) > 300 * 32 * 128 * 4 * 2
 
 
