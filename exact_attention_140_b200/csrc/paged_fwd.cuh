@@ -765,11 +765,10 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(empty(st));
     }
-    if (!ok) break;
 
     // ---- merge the key warps: rescale to the common references, sum, divide.
-    // (A warp whose wait ran out goes through the same barriers; all leave together
-    // below.)
+    // (A warp whose wait ran out goes through the same barriers with what it has; all
+    // leave together below, the error word set.)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
