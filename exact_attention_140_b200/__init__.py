@@ -673,8 +673,9 @@ def attention_paged(q, cache, table, kv_lens, cu_q=None, max_q=None, max_kv=None
         _index(cu_q, "cu_q", _i32, n + 1)
         max_q = Tq if max_q is None else min(max_q, Tq)
     else:
-        _need(n > 0 and Tq % n == 0 and max_q in (None, Tq // n), "without cu_q every sequence has Tq / n_seqs rows")
-        max_q = Tq // n
+        each = Tq // n if n > 0 else 0
+        _need(each * n == Tq and max_q in (None, each), "without cu_q every sequence has Tq / n_seqs rows")
+        max_q = each
     if max_kv is None:
         max_kv = width * cache.page_size
     dev = _on_current_device(q, table, kv_lens, cu_q, o, lse)

@@ -350,6 +350,7 @@ long long ragged_max_items(long long Tq, long long n_seqs, int Hq, int Hkv, int 
   const long long n = n_seqs < Tq ? n_seqs : Tq;
   return (Tq * ragged_rows_per_token(Hq, Hkv) + n * (block_rows - 1)) / block_rows;
 }
+constexpr long long kMaxItems = 1ll << 26;  // (item numbers times the ints of an item stay within 32 bits)
 // Whether the items are listed ahead: with many sequences, or where an SM has more
 // than one block to start (finding its item takes a block about 1 us, the list 5 us
 // and a launch: 4 prompts of up to 100 tokens 26 -> 18 us a call without it).
@@ -633,8 +634,9 @@ int attn_kv_read(const attn_kv_cache_t* cache, const int* table, int table_width
 long long attn_fwd_varlen_workspace_bytes(int Tq, int n_seqs, int Hq, int Hkv, int d) {
   if (Tq < 0 || n_seqs < 0 || Hq < 0 || Hkv < 1 || Hq % Hkv != 0 || !head_size_ok(d)) return -1;
   if (Tq == 0 || n_seqs == 0 || Hq == 0) return 0;
-  return ragged_plan_bytes(n_seqs, ragged_max_items(Tq, n_seqs, Hq, Hkv, ragged_block_rows(d, true)),
-                           ragged_rows_per_token(Hq, Hkv) > 1 ? Hkv : Hq);
+  const long long items = ragged_max_items(Tq, n_seqs, Hq, Hkv, ragged_block_rows(d, true));
+  const int nh = ragged_rows_per_token(Hq, Hkv) > 1 ? Hkv : Hq;
+  return items > kMaxItems ? -1 : ragged_plan_bytes(n_seqs, items, nh);
 }
 
 int attn_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse, int Tq, int Tk, int n_seqs,
@@ -655,6 +657,7 @@ int attn_fwd_varlen(const void* q, const void* k, const void* v, void* o, float*
                          reinterpret_cast<uintptr_t>(cu_k)) & 3u) != 0)
     return ATTN_ERR_MISALIGNED;
   const long long need = attn_fwd_varlen_workspace_bytes(Tq, n_seqs, Hq, Hkv, d);
+  if (need < 0) return ATTN_ERR_UNSUPPORTED;
   if (need > 0) {
     if (workspace == nullptr || workspace_bytes < need) return ATTN_ERR_INVALID_ARG;
     if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
@@ -694,6 +697,7 @@ long long attn_fwd_paged_workspace_bytes(const attn_kv_cache_t* cache, int Tq, i
   if (rc != ATTN_OK) return -1;
   if (cache->n_pages == 0) max_kv = 0;
   const PagedPlan pl = paged_plan(cache, Tq, n_seqs, max_q, Hq, max_kv);
+  if (pl.items > kMaxItems) return -1;
   return paged_space(pl, Tq, n_seqs, Hq, cache->Hkv, cache->d).all();
 }
 
@@ -715,6 +719,7 @@ int attn_fwd_paged(const void* q, const attn_kv_cache_t* cache, void* o, float* 
     return ATTN_ERR_MISALIGNED;
   if (cache->n_pages == 0) max_kv = 0;  // there is nothing to read
   const PagedPlan pl = paged_plan(cache, Tq, n_seqs, max_q, Hq, max_kv);
+  if (pl.items > kMaxItems) return ATTN_ERR_UNSUPPORTED;
   const PagedSpace sp = paged_space(pl, Tq, n_seqs, Hq, cache->Hkv, d);
   if (sp.all() > 0) {
     if (workspace == nullptr || workspace_bytes < sp.all()) return ATTN_ERR_INVALID_ARG;

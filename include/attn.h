@@ -484,8 +484,10 @@ int attn_kv_read(const attn_kv_cache_t *cache, const int *table, int table_width
  *              in a graph and replayed with other lengths
  *   workspace  DEVICE scratch, 16-byte aligned, of at least
  *              attn_fwd_varlen_workspace_bytes(Tq, n_seqs, Hq, Hkv, d) bytes (0 in a
- *              small call: workspace may be NULL), owned by the caller; calls
- *              that may overlap on the GPU need their own
+ *              small call: workspace may be NULL; -1 for invalid sizes, and for
+ *              more sequences or rows than one call takes, some 2^26 blocks of
+ *              rows), owned by the caller; calls that may overlap on the GPU need
+ *              their own
  * What one sequence holds never reaches another's rows, not even NaN.  Within a
  * sequence keys and values must be finite where a causal mask hides them (a
  * hidden NaN or infinity may reach rows of the same 128-row tile).

@@ -296,7 +296,7 @@ def test_graph_replayed_with_other_lengths(many):
     cq = su.starts([60] * n)
     T = 60 * n
     x = rand(torch, T, 4, 64, seed=2)
-    chunk = rand(torch, 4 * n, 24, 128, seed=3)  # 48 rows of 12 heads each and more than 64 in all of one
+    chunk = rand(torch, 4 * n, 24, 128, seed=3)  # max_q 8: 96 rows of a key/value head at most, so the block kernel
     cc = su.starts([4] * n)
 
     def step():
@@ -382,7 +382,7 @@ def test_paged_scales(n, scale, e4m3):
 
 
 def test_scales_of_far_apart_powers():
-    """Rows of an e4m3 cache whose scales differ by 2^60 and more, large values on keys of no weight among them."""
+    """Value rows of an e4m3 cache whose scales differ by 2^30 to 2^90."""
     torch, ea, su = setup()
     cache, table, ks, vs = su.make_cache(ea, [500], 16, 1, 128, True, seed=6)
     k_exp, v_exp = cache.tensors[2], cache.tensors[3]
@@ -393,10 +393,8 @@ def test_scales_of_far_apart_powers():
     v = cache.tensors[1][ids[i // 16], i % 16].view(torch.float8_e4m3fn).double() * su.pow2(e.long() - 127)[:, None, None]
     for n in (1, 100):
         q = rand(torch, n, 4, 128, seed=n)
-        # the keys with the large values all but hidden: their scores far below the others'
-        k2 = ks[0].clone()
         o, lse = ea.attention_paged(q, cache, table, su.i32(500))
-        su.check_attention(o, lse, su.attention(q, k2, v, True, 1 / math.sqrt(128)), 128)
+        su.check_attention(o, lse, su.attention(q, ks[0], v, True, 1 / math.sqrt(128)), 128)
 
 
 def test_queries_of_far_apart_sizes():
@@ -491,3 +489,99 @@ def test_tensors_elsewhere_are_refused():
         ea.attention_varlen(q.float(), q, q, su.i32(0, 5), su.i32(0, 5))
     with pytest.raises(TypeError):
         ea.attention_varlen(q, q, q, su.i32(0, 5).long(), su.i32(0, 5))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("d,new,cached", [(64, 1, 900), (128, 3, 700), (128, 40, 333), (128, 1024, 1500), (256, 300, 800),
+                                          (256, 512, 512)])
+def test_sequences_share_pages(d, new, cached, e4m3):
+    """A shared prefix: sequences whose table rows name the same pages, and a page that a row names twice."""
+    torch, ea, su = setup()
+    page = 64
+    cache, table, ks, vs = su.make_cache(ea, [cached], page, 2, d, e4m3, seed=d)
+    i = torch.arange(cached, device="cuda")
+    i = torch.where(i < 2 * page, i % page, i)  # the third sequence: its second page is its first again
+    twice = table[:1].clone()
+    twice[0, 1] = twice[0, 0]
+    both = torch.cat([table[:1], table[:1], twice]).contiguous()
+    q = rand(torch, 3 * new, 4, d, seed=2)
+    o, lse = ea.attention_paged(q, cache, both, su.i32(cached, cached - 5, cached))
+    su.no_device_error(ea)
+    for s, (k, v) in enumerate([(ks[0], vs[0]), (ks[0][:-5], vs[0][:-5]), (ks[0][i], vs[0][i])]):
+        r = slice(s * new, (s + 1) * new)
+        su.check_attention(o[r], lse[:, r], su.attention(q[r], k, v, True, 1 / math.sqrt(d)), d)
+
+
+def test_two_threads():
+    """Calls from two host threads, each on a stream of its own."""
+    import threading
+
+    torch, ea, su = setup()
+    cache, table, ks, vs = su.make_cache(ea, [700, 80], 32, 2, 128, True, seed=9)
+    kv = su.i32(700, 80)
+    x = rand(torch, 400, 8, 128, seed=1)
+    cu = su.i32(0, 150, 400)
+
+    def work():
+        o, lse = ea.attention_paged(x[:2], cache, table, kv)
+        c, _ = ea.attention_paged(x[:160], cache, table, kv)
+        p, _ = ea.attention_varlen(x, x[:, :2], x[:, 2:4], cu, cu, causal=True)
+        return o, lse, c, p
+
+    want = work()
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(stream):
+        with torch.cuda.stream(stream):
+            for _ in range(40):
+                if not all(torch.equal(a, b) for a, b in zip(work(), want)):
+                    wrong.append(stream)
+
+    threads = [threading.Thread(target=run, args=(torch.cuda.Stream(),)) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    su.no_device_error(ea)
+
+
+def test_prompt_step_captured_and_replayed():
+    """Write, a long chunk over an e4m3 cache (expanded, in windows) and its single-token form in one graph; a second
+    graph of the same calls replayed in turn with it."""
+    torch, ea, su = setup()
+    Hq, Hkv, d, page, T, cached = 8, 2, 128, 64, 300, 3000
+    cache, table, ks, vs = su.make_cache(ea, [cached], page, Hkv, d, True, seed=3)
+    ids = table[0].long()
+    x = [rand(torch, T, Hq + 2 * Hkv, d, seed=i) for i in (1, 2)]
+    pos = torch.arange(cached - T, cached, device="cuda")
+    slots = ids[pos // page] * page + pos % page
+    lens = su.i32(cached)
+
+    def step(y):
+        ea.kv_write(cache, y[:, Hq:Hq + Hkv], y[:, Hq + Hkv:], slots)
+        return ea.attention_paged(y[:, :Hq], cache, table, lens), ea.attention_paged(y[-1:, :Hq], cache, table, lens)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(x[0])
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [], []
+    for y in x:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step(y))
+        graphs.append(g)
+    for which in (0, 1, 0):
+        graphs[which].replay()
+        su.no_device_error(ea)
+        k, v = ks[0].clone(), vs[0].clone()
+        for new, c in ((x[which][:, Hq:Hq + Hkv], k), (x[which][:, Hq + Hkv:], v)):
+            val, ex = su.quantise(new)
+            c[-T:] = val * su.pow2(ex - 127).unsqueeze(-1)
+        (o, lse), (o1, l1) = outs[which]
+        ref = su.attention(x[which][:, :Hq], k, v, True, 1 / math.sqrt(d))
+        su.check_attention(o, lse, ref, d)
+        su.check_attention(o1, l1, su.attention(x[which][-1:, :Hq], k, v, True, 1 / math.sqrt(d)), d)

@@ -101,6 +101,7 @@ def varlen(**kw):
     (dict(n=200, Tq=300, ws=None), INVALID), (dict(n=200, Tq=300, wsb=16), INVALID),
     (dict(n=200, Tq=300, ws=P + 8), MISALIGNED), (dict(o=P + 8), MISALIGNED),
     (dict(lse=P + 2), MISALIGNED), (dict(cq=P + 1), MISALIGNED), (dict(qs=100), INVALID), (dict(ks=260), MISALIGNED),
+    (dict(Tq=(1 << 31) - 1, n=(1 << 31) - 1), UNSUPPORTED),
     (dict(Tq=0), OK), (dict(n=0), OK), (dict(Hq=0), OK)])
 def test_varlen_refusals(kw, status):
     assert varlen(**kw) == status
@@ -110,6 +111,7 @@ def test_varlen_workspace():
     f = ea.attn_fwd_varlen_workspace_bytes
     assert f(-1, 1, 4, 2, 128) == f(8, 1, 3, 2, 128) == f(8, 1, 4, 0, 128) == f(8, 1, 4, 2, 96) == -1
     assert f(0, 1, 4, 2, 128) == f(8, 0, 4, 2, 128) == 0
+    assert f((1 << 31) - 1, (1 << 31) - 1, 4, 2, 128) == -1  # more blocks than one call takes
     assert f(1000, 128, 32, 8, 128) == (32 * ((4000 + 128 * 255) // 256) + 255) // 256 * 256
     assert f(1000, 2, 32, 8, 128) == 0  # at most a block per SM: each finds its own item
     # otherwise a list of 32-byte items: blocks of 256 rows (128 at other head sizes), groups of 4 stacked
@@ -145,6 +147,7 @@ def test_paged_workspace():
     f = ea.attn_fwd_paged_workspace_bytes
     c = cache(Hkv=8)
     assert f(c, 0, 1, 1, 32, 64) == 0 and f(c, 4, 4, 1, 33, 64) == -1 and f(c, 4, 4, 5, 32, 64) == -1
+    assert f(c, (1 << 31) - 1, (1 << 31) - 1, 32, 32, 64) == -1  # more blocks than one call takes
     assert f(c, 4, 4, 1, 32, 192) == 0  # a cluster of blocks per sequence and head
     # a count per sequence, and two partial blocks of 8 rows for each of the 50 * 8 * 3 units, or
     # of the 2 blocks that an SM holds where those are fewer
