@@ -79,11 +79,13 @@ __device__ __forceinline__ uint32_t e4m3_row_exponent(uint32_t amax_bits) {
 //
 // A block takes `tokens` neighbouring tokens: their cosines and sines once, into
 // shared memory, then set after set of rows (one row per lane group), each for all
-// the tokens, four tokens' loads on their way together.  A lane group stays with
-// its head for a set, so weights and pointers are loop constants.  Between HBM and
-// the issue rate: 8192 tokens of 32 + 8 heads of 128 take 39 us (4.3 TB/s); with a
-// token's rows side by side and the halves exchanged by shuffles, at 1.4 times the
-// instructions, 53 us.
+// the tokens.  Every thread copies its own pieces of the next three steps into a
+// ring in shared memory that no other thread touches, so loads go on under the
+// arithmetic and across sets, and nothing is waited for but the thread's own
+// copies.  A lane group stays with its head for a set, so weights and pointers are
+// loop constants.  8192 tokens of 32 + 8 heads of 128 take 35 us (4.8 TB/s); with
+// four tokens' loads into registers and no ring 39, with a ring of 8 steps 36.7,
+// with more threads a SM 48 (their registers spill).
 constexpr int kHeadRowsMaxTokens = 16, kHeadRowsAhead = 4, kHeadRowsBps = 4;
 enum : int { kRowsDense = 0, kRowsBf16Cache = 1, kRowsE4m3Cache = 2 };
 
@@ -93,6 +95,7 @@ __global__ void __launch_bounds__(256, kHeadRowsBps) head_rows_kernel(const Head
   constexpr int NG = 256 / G;        // rows of a set
   constexpr int U = kHeadRowsAhead;
   __shared__ __align__(16) float s_cos[kHeadRowsMaxTokens][D / 2], s_sin[kHeadRowsMaxTokens][D / 2];
+  __shared__ uint2 s_in[U][2][256];  // (only the thread itself touches its places)
   const int gid = threadIdx.x / G, l = threadIdx.x % G;
   const long long t0 = (long long)blockIdx.x * tokens;
   const int nt = p.T - t0 < tokens ? (int)(p.T - t0) : tokens;
@@ -102,6 +105,39 @@ __global__ void __launch_bounds__(256, kHeadRowsBps) head_rows_kernel(const Head
   const bool rotated = 4 * l < half;
   const int ea = INTERLEAVED || half == 0 ? 8 * l : (rotated ? 4 * l : p.rot + 8 * (l - half / 4));
   const int eb = !INTERLEAVED && rotated ? half + 4 * l : ea + 4;
+  // the warp's steps: set after set, the tokens of each in turn
+  const int r_first = (int)blockIdx.y * NG + gid, r_warp = r_first - (int)(threadIdx.x & 31) / G;
+  const int r_step = (int)gridDim.y * NG;
+  const int steps = r_warp < rows ? ((rows - r_warp + r_step - 1) / r_step) * nt : 0;
+  // loads run U - 1 steps ahead of the arithmetic
+  const uint32_t slot0 = ptx::smem_u32(&s_in[0][0][threadIdx.x]);
+  constexpr uint32_t SLOT = sizeof(uint2) * 2 * 256, SIDE = sizeof(uint2) * 256;
+  int lr = r_first - r_step, li = nt, lk = 0;
+  const __nv_bfloat16* lp = nullptr;
+  long long l_step = 0;
+  auto load = [&]() {
+    if (lk < steps) {
+      if (li == nt) {
+        li = 0;
+        lr += r_step;
+        const bool is_q = lr < p.Hq, is_v = MODE != kRowsDense && lr >= p.Hq + p.Hkv;
+        const int h = is_q ? lr : (is_v ? lr - p.Hq - p.Hkv : lr - p.Hq);
+        l_step = is_q ? p.q_stride : (is_v ? p.v_stride : p.k_stride);
+        lp = (is_q ? p.q : (is_v ? p.v : p.k)) + t0 * l_step + (long long)h * D;
+      }
+      if (lr < rows) {
+        const uint32_t at = slot0 + (uint32_t)(lk % U) * SLOT;
+        ptx::cp_async8(at, lp + ea);
+        ptx::cp_async8(at + SIDE, lp + eb);
+      }
+      lp += l_step;
+      ++li;
+      ++lk;
+    }
+    ptx::cp_async_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < U - 1; ++i) load();
   if (half > 0) {
     for (int i = threadIdx.x; i < nt * half; i += 256) {
       const int t = i / half, j = i - t * half;
@@ -113,12 +149,10 @@ __global__ void __launch_bounds__(256, kHeadRowsBps) head_rows_kernel(const Head
     }
     __syncthreads();
   }
-  for (int r = blockIdx.y * NG + gid; r - gid < rows; r += gridDim.y * NG) {
-    if (r - (int)(threadIdx.x & 31) / G >= rows) break;  // none of the warp's rows is there
+  int k = 0;
+  for (int r = r_first; k < steps; r += r_step) {
     const bool live = r < rows, is_q = r < p.Hq, is_v = MODE != kRowsDense && r >= p.Hq + p.Hkv;
     const int h = is_q ? r : (is_v ? r - p.Hq - p.Hkv : r - p.Hq);
-    const long long in_step = is_q ? p.q_stride : (is_v ? p.v_stride : p.k_stride);
-    const __nv_bfloat16* in = (is_q ? p.q : (is_v ? p.v : p.k)) + t0 * in_step + (long long)h * D;
     // where dense rows go; the cache's rows follow the tokens' slots
     const bool dense = MODE == kRowsDense || is_q;
     const long long out_step = is_q ? p.q_out_stride : p.k_out_stride;
@@ -130,83 +164,72 @@ __global__ void __launch_bounds__(256, kHeadRowsBps) head_rows_kernel(const Head
       unpack8(make_uint4(wa.x, wa.y, wb.x, wb.y), wf);
     }
     const bool turn = rotated && !is_v;
-    for (int i0 = 0; i0 < nt; i0 += U) {
-      uint2 ra[U], rb[U];
+#pragma unroll 1
+    for (int i = 0; i < nt; ++i, ++k) {
+      load();
+      ptx::cp_async_wait<U - 1>();
+      const uint2 ra = s_in[k % U][0][threadIdx.x], rb = s_in[k % U][1][threadIdx.x];
+      float x[8];
+      unpack8(make_uint4(ra.x, ra.y, rb.x, rb.y), x);
+      // (the shuffles below run on every lane: all 32 lanes of a warp stay together)
+      if (p.q_weight != nullptr || p.k_weight != nullptr) {
+        float ss = 0.f;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        ra[u] = rb[u] = make_uint2(0u, 0u);
-        if (live && i0 + u < nt) {
-          ra[u] = *reinterpret_cast<const uint2*>(in + ea);
-          rb[u] = *reinterpret_cast<const uint2*>(in + eb);
-        }
-        in += in_step;
+        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+        for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float inv = w != nullptr ? rsqrtf(ss * (1.f / D) + p.eps) : 1.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= wf[e] * inv;
       }
+      if (turn) {
+        const float4 c4 = *reinterpret_cast<const float4*>(&s_cos[i][4 * l]);
+        const float4 s4 = *reinterpret_cast<const float4*>(&s_sin[i][4 * l]);
+        const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + u;
-        if (i >= nt) break;  // (the whole block)
-        float x[8];
-        unpack8(make_uint4(ra[u].x, ra[u].y, rb[u].x, rb[u].y), x);
-        // (the shuffles below run on every lane: all 32 lanes of a warp stay together)
-        if (p.q_weight != nullptr || p.k_weight != nullptr) {
-          float ss = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-          for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          const float inv = w != nullptr ? rsqrtf(ss * (1.f / D) + p.eps) : 1.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= wf[e] * inv;
+        for (int e = 0; e < 4; ++e) {
+          constexpr int A = INTERLEAVED ? 2 : 1, B = INTERLEAVED ? 1 : 4;  // pair e: elements A e and A e + B
+          const float a0 = x[A * e], b0 = x[A * e + B];
+          x[A * e] = a0 * c[e] - b0 * s[e];
+          x[A * e + B] = b0 * c[e] + a0 * s[e];
         }
-        if (turn) {
-          const float4 c4 = *reinterpret_cast<const float4*>(&s_cos[i][4 * l]);
-          const float4 s4 = *reinterpret_cast<const float4*>(&s_sin[i][4 * l]);
-          const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            constexpr int A = INTERLEAVED ? 2 : 1, B = INTERLEAVED ? 1 : 4;  // pair e: elements A e and A e + B
-            const float a0 = x[A * e], b0 = x[A * e + B];
-            x[A * e] = a0 * c[e] - b0 * s[e];
-            x[A * e + B] = b0 * c[e] + a0 * s[e];
-          }
+      }
+      if (dense) {
+        if (live) {
+          const uint4 y = pack8(x);
+          *reinterpret_cast<uint2*>(out + ea) = make_uint2(y.x, y.y);
+          *reinterpret_cast<uint2*>(out + eb) = make_uint2(y.z, y.w);
         }
-        if (dense) {
-          if (live) {
+        out += out_step;
+      }
+      if constexpr (MODE != kRowsDense) {
+        long long slot = __ldg(p.slots + t0 + i);
+        if (slot >= p.n_slots) {
+          if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.err, kErrIndex);
+          slot = -1;
+        }
+        const bool store = live && !is_q && slot >= 0;
+        const long long row = slot * p.Hkv + h;
+        if constexpr (MODE == kRowsBf16Cache) {
+          if (store) {
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? p.v_pages : p.k_pages) + row * D;
             const uint4 y = pack8(x);
-            *reinterpret_cast<uint2*>(out + ea) = make_uint2(y.x, y.y);
-            *reinterpret_cast<uint2*>(out + eb) = make_uint2(y.z, y.w);
+            *reinterpret_cast<uint2*>(dst + ea) = make_uint2(y.x, y.y);
+            *reinterpret_cast<uint2*>(dst + eb) = make_uint2(y.z, y.w);
           }
-          out += out_step;
-        }
-        if constexpr (MODE != kRowsDense) {
-          long long slot = __ldg(p.slots + t0 + i);
-          if (slot >= p.n_slots) {
-            if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.err, kErrIndex);
-            slot = -1;
-          }
-          const bool store = live && !is_q && slot >= 0;
-          const long long row = slot * p.Hkv + h;
-          if constexpr (MODE == kRowsBf16Cache) {
-            if (store) {
-              __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? p.v_pages : p.k_pages) + row * D;
-              const uint4 y = pack8(x);
-              *reinterpret_cast<uint2*>(dst + ea) = make_uint2(y.x, y.y);
-              *reinterpret_cast<uint2*>(dst + eb) = make_uint2(y.z, y.w);
-            }
-          } else {
-            uint32_t a = 0u;  // the largest magnitude, by its bits
+        } else {
+          uint32_t a = 0u;  // the largest magnitude, by its bits
 #pragma unroll
-            for (int e = 0; e < 8; ++e) a = max(a, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+          for (int e = 0; e < 8; ++e) a = max(a, __float_as_uint(x[e]) & 0x7FFFFFFFu);
 #pragma unroll
-            for (int o = G / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-            const uint32_t e = e4m3_row_exponent(a);
-            const float m = __uint_as_float((e == kExpNaN ? 127u : 254u - e) << 23);  // 2^-(e - 127)
-            if (store) {
-              unsigned char* dst = static_cast<unsigned char*>(is_v ? p.v_pages : p.k_pages) + row * D;
-              *reinterpret_cast<uint32_t*>(dst + ea) = ptx::pack_e4m3x4(x[0] * m, x[1] * m, x[2] * m, x[3] * m);
-              *reinterpret_cast<uint32_t*>(dst + eb) = ptx::pack_e4m3x4(x[4] * m, x[5] * m, x[6] * m, x[7] * m);
-              if (l == 0) (is_v ? p.v_exp : p.k_exp)[row] = (unsigned char)e;
-            }
+          for (int o = G / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+          const uint32_t e = e4m3_row_exponent(a);
+          const float m = __uint_as_float((e == kExpNaN ? 127u : 254u - e) << 23);  // 2^-(e - 127)
+          if (store) {
+            unsigned char* dst = static_cast<unsigned char*>(is_v ? p.v_pages : p.k_pages) + row * D;
+            *reinterpret_cast<uint32_t*>(dst + ea) = ptx::pack_e4m3x4(x[0] * m, x[1] * m, x[2] * m, x[3] * m);
+            *reinterpret_cast<uint32_t*>(dst + eb) = ptx::pack_e4m3x4(x[4] * m, x[5] * m, x[6] * m, x[7] * m);
+            if (l == 0) (is_v ? p.v_exp : p.k_exp)[row] = (unsigned char)e;
           }
         }
       }
