@@ -12,9 +12,11 @@ namespace attn {
 
 // Packed sequences (one-block-per-item kernel, RAGGED configurations): each
 // block picks its work item, or takes it from a list in device memory, items of 8
-// ints: seq (-1: none), block, q0, nq, k0, nk, 0, 0.
+// ints: seq (-1: none), block, q0, nq, k0, nk, 0, 0; or the list is of pieces of
+// items, each with its head, key tiles and the slot of its partial rows.
 struct RaggedParams {
   PlanParams seqs;   // max_items: items that the launch's grid has room for
+  bool pieces;       // the list is of pieces: o_part [slots][block rows][D], lse_part [slots][block rows]
   const int* table;  // paged: page table [n_seqs, table_width]
   int table_width, page_shift, n_pages;
   const unsigned char *k_exp, *v_exp;  // e4m3 cache: exponent bytes [n_pages, page_size, Hkv]

@@ -83,17 +83,30 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
   int qb, hy, b, split;
   int nq = p.Nq, nk_all = p.Nk;                       // query rows and keys of the item's sequence
   [[maybe_unused]] int q_base = 0, k_base = 0, seq = 0;  // RAGGED: its first query token and key, its index
+  [[maybe_unused]] int slot = -1, kv_begin = 0, kv_end = 0;  // RAGGED: its partial rows (-1: none), its keys
   if constexpr (Cfg::RAGGED != 0) {
     // bands of heads as below, the listed items (longest first) within a band
     ptx::grid_dep_launch();
-    split = (int)blockIdx.x % p.n_splits;
+    split = (int)blockIdx.x % p.n_splits;  // (1 with pieces)
     const int L = (int)blockIdx.x / p.n_splits, per = p.band * p.rg.seqs.max_items;
-    const int bi = L / per, within = L - bi * per;
+    const int bi = p.rg.pieces ? 0 : L / per, within = L - bi * per;
     const int bsz = p.nh - bi * p.band < p.band ? p.nh - bi * p.band : p.band;
     const int item = within / bsz;
+    hy = bi * p.band + within % bsz;
     int4 i0;
     int2 i1;
-    if (p.rg.seqs.plan == nullptr) {
+    if (p.rg.pieces) {
+      ptx::grid_dep_wait();
+      const int4* it = reinterpret_cast<const int4*>(p.rg.seqs.plan) + 3 * L;
+      i0 = __ldcg(it);
+      const int4 i2 = __ldcg(it + 1);
+      const int2 i3 = __ldcg(reinterpret_cast<const int2*>(it + 2));
+      i1 = make_int2(i2.x, i2.y);
+      hy = i2.z;
+      slot = i2.w;
+      kv_begin = i3.x * BN;
+      kv_end = i3.y;
+    } else if (p.rg.seqs.plan == nullptr) {
       int* s_item = reinterpret_cast<int*>(sgen);  // (nothing has been loaded yet)
       if (warp == 0) {
         const bool there = ragged_pick(p.rg.seqs, item, i0, i1);
@@ -119,7 +132,6 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
       i1 = __ldcg(reinterpret_cast<const int2*>(p.rg.seqs.plan) + 2 + 4 * item);
     }
     if (i0.x < 0) return;
-    hy = bi * p.band + within % bsz;
     b = 0;
     // (a shuffle from lane 0 shows the compiler that the warp agrees on them, so
     // that loops and descriptors stay in uniform registers)
@@ -130,7 +142,17 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
     nq = uni(i0.w);
     k_base = uni(i1.x);
     nk_all = uni(i1.y);
-    if (split > 0 && split * p.kv_chunk >= nk_all) return;  // no such window
+    if (p.rg.pieces) {
+      hy = uni(hy);
+      slot = uni(slot);
+      kv_begin = uni(kv_begin);
+      kv_end = (long long)uni(kv_end) * BN < nk_all ? uni(kv_end) * BN : nk_all;
+    } else {
+      kv_begin = split * p.kv_chunk;
+      if (split > 0 && kv_begin >= nk_all) return;  // no such window
+      kv_end = nk_all - kv_begin < p.kv_chunk ? nk_all : kv_begin + p.kv_chunk;
+      slot = nk_all > p.kv_chunk ? split : -1;
+    }
   } else if (p.band > 0) {
     // longest-first within bands of (batch, head) pairs: a band's K/V stay in
     // L2 while its blocks run, and the hardware hands out blocks in this
@@ -152,8 +174,8 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
     split = (int)blockIdx.z % p.n_splits;
   }
   // key window of this block: [kv0, kv0 + nk), `shift` keys after it
-  const int kv0 = split * p.kv_chunk;
-  const int nk = nk_all - kv0 < p.kv_chunk ? nk_all - kv0 : p.kv_chunk;
+  const int kv0 = Cfg::RAGGED != 0 ? kv_begin : split * p.kv_chunk;
+  const int nk = Cfg::RAGGED != 0 ? kv_end - kv_begin : (nk_all - kv0 < p.kv_chunk ? nk_all - kv0 : p.kv_chunk);
   const int shift = nk_all - kv0 - nk;
   const int kh = g > 1 ? hy : hy / p.group;
   const int q0 = qb * BM * NQT;
@@ -221,9 +243,9 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
     const int t = warp >> 2, wq = warp & 3;
     int ia, ib;
     tile_rows(t, ia, ib);
-    const int prow = q0 + t * BM + wq * 32 + lane;  // this thread's (packed) tile row
-    const int row = prow / g;                         // its query row
-    const int h = g > 1 ? kh * g + (prow - row * g) : hy;
+    const int prow_packed = q0 + t * BM + wq * 32 + lane;  // this thread's (packed) tile row
+    const int row = prow_packed / g;                         // its query row
+    const int h = g > 1 ? kh * g + (prow_packed - row * g) : hy;
     const int nt = n_kv[t];
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t o_taddr = tmem + lane_off + (uint32_t)(Cfg::O_COL0 + t * D);
@@ -408,7 +430,7 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
       if constexpr (Cfg::RAGGED != 0) {
         tok = (long long)q_base + row;
         lse_at = (long long)h * p.rg.seqs.Tq + tok;
-        final_out = p.o_part == nullptr || nk_all <= p.kv_chunk;  // (one window only)
+        final_out = slot < 0;
       } else {
         tok = (long long)b * p.Nq + row;
         lse_at = ((long long)b * p.Hq + h) * p.Nq + row;
@@ -436,10 +458,11 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
         }
         if (store && p.lse != nullptr) p.lse[lse_at] = lse;
       } else {
-        // split-KV partial of window `split`: fp32 O_s and LSE_s
+        // partial of window `split`, or of a piece: fp32 O_s and LSE_s
         long long prow, plse;
         if constexpr (Cfg::RAGGED != 0) {
-          prow = plse = ((long long)split * p.rg.seqs.Tq + tok) * p.Hq + h;
+          prow = plse = p.rg.pieces ? (long long)slot * (BM * NQT) + (prow_packed - q0)
+                                    : ((long long)slot * p.rg.seqs.Tq + tok) * p.Hq + h;
         } else {
           const long long zs = (long long)split * p.B + b;
           prow = (zs * p.Nq + row) * p.Hq + h;

@@ -934,9 +934,9 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
 // (fp32, normalised by its own sum) with its LSE (natural log) in lse_part.
 //   LSE = ln sum_w exp(LSE_w),   O = sum_w exp(LSE_w - LSE) O_w
 // (parts without a visible key have O_w = 0, LSE_w = -inf and weigh nothing.)  Bound
-// by the latency of one read from L2: the first eight parts' rows and all parts'
-// LSE are requested together, and the row of a lane is one wide load.
-template <int D, class Slot>
+// by the latency of one read from L2: the rows of the first AHEAD parts and all
+// parts' LSE are requested together, and the row of a lane is one wide load.
+template <int D, int AHEAD, class Slot>
 __device__ __forceinline__ void merge_parts(const float* o_part, const float* lse_part, int S, Slot slot, int lane,
                                             __nv_bfloat16* o, float* lse) {
   constexpr int PER = D / 32;
@@ -960,7 +960,6 @@ __device__ __forceinline__ void merge_parts(const float* o_part, const float* ls
     }
     return x;
   };
-  constexpr int AHEAD = 8;
   Piece y[AHEAD];
   float ls = lane < S ? __ldcg(lse_part + slot(lane)) : -INFINITY;
 #pragma unroll
@@ -1053,31 +1052,71 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p,
   const long long a = base + in_seq, i0 = a / share, i1 = (a + units - 1) / share;
   if (i0 == i1) return;
   const int S = (int)(i1 - i0 + 1);
-  merge_parts<D>(p.o_part, p.lse_part, S,
+  merge_parts<D, 8>(p.o_part, p.lse_part, S,
                  [&](int w) -> long long { return (2 * (i0 + w) + (w == S - 1 ? 0 : 1)) * block_rows + r; }, lane,
                  p.o + i * D, p.lse != nullptr ? p.lse + (long long)h * p.Tq + t : nullptr);
 }
 
-// Merge of the key windows of the tcgen05 kernel's items, parts
-// [window][Tq][Hq]; a sequence of one window is final already.
-struct WindowParams : PagedSeqs {
+// Merge of what the tcgen05 kernel left as partial rows: of the key windows of its
+// items, parts [window][Tq][Hq] (a sequence of one window is final already), or of
+// the items it took in pieces, whose parts are the runs that the pair of item and
+// head lies in.  A block takes a token, a warp some of its heads (grid y shares them
+// out too): the look-ups (sequence, item, its place in the line) wait for one
+// another, so a warp makes them once for its heads (1671 tokens of 32 heads of 128,
+// cold caches: 60 us with a warp per head, 30 so).
+struct LongParams : PagedSeqs {
   __nv_bfloat16* o;
   float* lse;
-  int Hq, window;
+  int Hq, window;  // window > 0: windows
+  int rows_per_token, block_rows, nh, max_items;
+  const long long* lin;
+  const int* first;
   const float *o_part, *lse_part;
 };
 template <int D>
-__global__ void __launch_bounds__(256) window_combine_kernel(const WindowParams p) {
-  const long long i = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int t = (int)(i / p.Hq), h = (int)(i - (long long)t * p.Hq);
+__global__ void __launch_bounds__(256) long_combine_kernel(const LongParams p) {
+  const int t = (int)blockIdx.x, lane = threadIdx.x & 31;
   SeqRange sr;
-  const bool several = t < p.Tq && paged_seq_of(p, t, sr) >= 0 && sr.len > p.window;
+  const int s = paged_seq_of(p, t, sr);
   ptx::grid_dep_wait();
-  if (!several) return;
-  const long long all = (long long)p.Tq * p.Hq;
-  merge_parts<D>(p.o_part, p.lse_part, (sr.len + p.window - 1) / p.window,
-                 [&](int w) -> long long { return w * all + i; }, threadIdx.x & 31, p.o + i * D,
-                 p.lse != nullptr ? p.lse + (long long)h * p.Tq + t : nullptr);
+  if (s < 0) return;
+  const int h0 = (int)(blockIdx.y * 8 + (threadIdx.x >> 5)), h_step = (int)gridDim.y * 8;
+  auto merge = [&](int h, int S, auto slot) {
+    merge_parts<D, 4>(p.o_part, p.lse_part, S, slot, lane, p.o + ((long long)t * p.Hq + h) * D,
+                   p.lse != nullptr ? p.lse + (long long)h * p.Tq + t : nullptr);
+  };
+  if (p.window > 0) {
+    if (sr.len <= p.window) return;
+    const int S = (sr.len - 1) / p.window + 1;
+    const long long all = (long long)p.Tq * p.Hq;
+    for (int h = h0; h < p.Hq; h += h_step)
+      merge(h, S, [&](int w) -> long long { return w * all + (long long)t * p.Hq + h; });
+    return;
+  }
+  const int g = p.rows_per_token, shift = 31 - __clz(p.block_rows);
+  const long long r0 = (long long)(t - sr.q0) * g;  // (the g rows of a token are in one block)
+  const long long item = __ldcg(p.first + s) + (r0 >> shift);
+  if (item >= __ldcg(p.first + p.n_seqs)) return;
+  const long long front = __ldcg(p.lin + item), c = __ldcg(p.lin + item + 1) - front;
+  const long long share = __ldcg(p.lin + p.max_items + 1);
+  const bool small = (front + c) * p.nh < (1ll << 31) && share < (1ll << 31);
+  for (int h = h0; h < p.Hq; h += h_step) {
+    const int hy = h / g;
+    int v0, S;  // the first run, and the runs
+    if (small) {
+      const PieceRuns<unsigned> x = piece_runs<unsigned>((unsigned)front * (unsigned)p.nh + (unsigned)hy * (unsigned)c,
+                                                         (unsigned)c, (unsigned)share);
+      v0 = (int)x.first;
+      S = (int)(x.last - x.first) + 1;
+    } else {
+      const PieceRuns<long long> x = piece_runs<long long>(front * p.nh + hy * c, c, share);
+      v0 = (int)x.first;
+      S = (int)(x.last - x.first) + 1;
+    }
+    if (S == 1) continue;
+    const int row = (int)((r0 + h - hy * g) & (p.block_rows - 1));
+    merge(h, S, [&](int w) -> long long { return ((long long)(2 * (v0 + w) + (w == S - 1 ? 0 : 1)) << shift) + row; });
+  }
 }
 
 }  // namespace attn

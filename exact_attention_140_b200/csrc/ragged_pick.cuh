@@ -8,6 +8,8 @@
 namespace attn {
 
 constexpr int kPlanItem = 8;   // ints of an item
+constexpr int kPlanPiece = 12;  // ints of a piece of an item
+constexpr int kPieceSeqs = 1024, kPieceItems = 1024;  // sequences and items that are cut into pieces, at most
 constexpr int kPickPerLane = 4, kPickSeqs = 32 * kPickPerLane;
 
 struct PlanParams {
@@ -37,6 +39,36 @@ ATTN_HD int ragged_items_from(long long c, int nq, int nk, int nb, int bn, int s
   const long long L = below - nk + nq;
   if (L > nq - 1) return 0;
   return L <= 0 ? nb : nb - (int)((L * g) >> shift);
+}
+
+// Pieces.  The key tiles of all (item, head) pairs stand in one line, item by item,
+// heads within an item, and are cut into runs of `share` tiles.  A pair with the
+// tiles [a, a + c) lies in the runs first .. last; the piece in run v holds its tiles
+// [lo, hi), and unless it is the whole pair its rows are partial, in slot 2 v where
+// the pair ends in the run and 2 v + 1 where it goes on: a run holds one of each
+// at most.
+// T: long long, or unsigned where a line fits it (its division is much shorter).
+template <class T>
+struct PieceRuns {
+  T first, last;
+};
+template <class T>
+ATTN_HD PieceRuns<T> piece_runs(T a, T c, T share) {
+  const T first = a / share;
+  return PieceRuns<T>{first, c > 0 ? (a + c - 1) / share : first};
+}
+template <class T>
+struct Piece {
+  T lo, hi;
+  int slot;  // -1: whole
+};
+template <class T>
+ATTN_HD Piece<T> piece_of(T a, T c, T share, PieceRuns<T> r, T v) {
+  Piece<T> x;
+  x.lo = (v * share > a ? v * share : a) - a;
+  x.hi = ((v + 1) * share < a + c ? (v + 1) * share : a + c) - a;
+  x.slot = r.first == r.last ? -1 : (int)(2 * v + (v == r.last ? 0 : 1));
+  return x;
 }
 
 #ifdef __CUDACC__

@@ -133,12 +133,13 @@ int launch_kv_read_cache(KvReadParams& p, const attn_kv_cache_t* cache, const in
 // ---------------------------------------------------------------- paged attention
 // How a paged call runs.  Few rows per sequence: paged_fwd_kernel, `size` its
 // block configuration, `blocks` its grid.  More (items > 0): the tcgen05 kernel
-// over listed items, each sequence's keys cut into n_windows windows where the
-// items are too few for the GPU.  expand > 0: an e4m3 cache read back into bf16
-// rows first, `expand` of them for each sequence.
+// over items, each sequence's keys cut into n_windows windows where the items are
+// few, or over pieces of items of equal cost in sum.
+// expand > 0: an e4m3 cache read back into bf16 rows first, `expand` of them for each
+// sequence.
 struct PagedPlan {
   int size, block_rows, unit, row_tiles, blocks;
-  bool cluster;
+  bool cluster, pieces;
   long long items;
   int window, n_windows, expand;
 };
@@ -148,6 +149,7 @@ int ragged_rows_per_token(int Hq, int Hkv);
 long long ragged_plan_bytes(long long n_seqs, long long items, int nh);
 
 constexpr int kSms = 148;  // SMs of a B200: the grids and their workspace go by it
+constexpr int kPieceBlocks = 2 * kSms;  // with more blocks than that whole items are as good
 // Rows of a block: one tile of 8 rows a warp, then two where the accumulators fit
 // (d = 256: one), then more warps along the rows.
 constexpr int kPagedSizes = 4;
@@ -175,31 +177,57 @@ PagedGeometry paged_geometry(int d, bool e4m3, int size) {
 
 constexpr long long kExpandBytes = 1ll << 30;  // of workspace for expanded keys and values, at most
 
+// Whole items, key windows or pieces, by an estimate in us from what the host
+// knows.  A block takes 16 ns a key (21 at d = 256) and 9.6 us besides.  Windows
+// (one: whole items): the waves of blocks, and writing and merging the partial
+// rows (4 TB/s, 5 us to begin with); with equal lengths they fit, and need no list.
+// Pieces: the mean of an SM, 24 us of fixed costs and the list, two partial blocks an
+// SM, and the look-ups of the merge.  From two waves on the mean of a causal chunk
+// counts; the sequences of a batch differ, so less than the longest on average is
+// assumed, and that long and short blocks pair off in part.
+// Measured, us by windows / by pieces / by the estimates (32/8 heads of 128, bf16,
+// one call after another): 1 x 8192 keys, 2048 new tokens 240 / 287 / 248, 272; 4 x up
+// to 12000, 256 tokens 204 / 148 / 202, 172; the same, 512 tokens 302 / 272 / 340, 283;
+// 1 x 32768, 256 tokens 156 / 155 / 154, 160; the same, 2048 tokens 991 / 950 / 1035, 952.
+// With many items pieces gain nothing, and those of one head drift apart and read its
+// keys from HBM more often: 4 x up to 8192, 2048 tokens 501 / 571.
+void plan_long(PagedPlan* pl, long long blocks, int Tq, int n_seqs, int max_q, int Hq, int max_kv, int block_rows, int d) {
+  const double ns = d == 256 ? 0.021 : 0.016, mean_kv = max_kv - 0.5 * (max_q < max_kv ? max_q : max_kv);
+  long long want = 1;
+  double best = 0.0;
+  for (long long n = 1; n <= 16 && (n == 1 || max_kv / n >= 512); ++n) {
+    const long long waves = (blocks * n + kSms - 1) / kSms;
+    const double keys = (waves == 1 ? max_kv : mean_kv * (n_seqs > 1 ? 0.85 : 1.0)) / (double)n;
+    const double t = waves * (keys * ns + 9.6) + (n == 1 ? 0.0 : 5.0 + 2.0 * n * Tq * Hq * d * 4 / 4e6);
+    if (n == 1 || t < best) {
+      best = t;
+      want = n;
+    }
+  }
+  const double mean = blocks * mean_kv * (n_seqs > 1 ? 0.75 : 1.0) / kSms;
+  const double pieces = (mean < 512.0 ? 512.0 : mean) * ns + 24.0 + 2.0 * 2 * kSms * block_rows * d * 4 / 4e6 +
+                        5e-4 * Tq * Hq;
+  pl->n_windows = 1;
+  if (blocks <= kPieceBlocks && pl->items <= kPieceItems && n_seqs <= kPieceSeqs && pieces < best) {
+    pl->pieces = true;
+    return;
+  }
+  const long long w = (((long long)max_kv + want - 1) / want + 127) / 128 * 128;
+  pl->window = (int)(w < 128 ? 128 : w);
+  if (max_kv > pl->window) pl->n_windows = (int)(((long long)max_kv + pl->window - 1) / pl->window);
+}
 PagedPlan paged_plan(const attn_kv_cache_t* c, int Tq, int n_seqs, int max_q, int Hq, int max_kv) {
   PagedPlan pl = {};
   const int Hkv = c->Hkv;
   const long long rows = (long long)max_q * (Hq / Hkv);
   if (rows > 64 && c->n_pages > 0) {
     pl.items = ragged_max_items(Tq, n_seqs, Hq, Hkv, ragged_block_rows(c->d, false));
-    const int g = ragged_rows_per_token(Hq, Hkv);
-    // Windows by an estimate in key times (one block, 256 rows, about 16 ns a key):
-    // the waves of blocks times a window's keys and a block's fixed cost, and
-    // writing and merging the partial rows (about 4 TB/s, 5 us to begin with).
-    const long long blocks = ((long long)Tq * g / ragged_block_rows(c->d, false) + (n_seqs + 1) / 2) * (g > 1 ? Hkv : Hq);
-    long long want = 1;
-    double best = 0.0;
-    for (long long n = 1; n <= 16 && (n == 1 || max_kv / n >= 512); ++n) {
-      const double waves = (double)((blocks * n + kSms - 1) / kSms);
-      const double merge = n == 1 ? 0.0 : 300.0 + 2.0 * n * Tq * Hq * c->d * 4 / 64000.0;
-      const double t = waves * ((double)max_kv / n + 600.0) + merge;
-      if (n == 1 || t < best) {
-        best = t;
-        want = n;
-      }
-    }
-    const long long w = (((long long)max_kv + want - 1) / want + 127) / 128 * 128;
-    pl.window = (int)(w < 128 ? 128 : w);
-    pl.n_windows = max_kv > pl.window ? (int)(((long long)max_kv + pl.window - 1) / pl.window) : 1;
+    const int g = ragged_rows_per_token(Hq, Hkv), rows_block = ragged_block_rows(c->d, false);
+    // blocks: known where every sequence has max_q tokens
+    long long n_items = (long long)n_seqs * max_q == Tq ? (long long)n_seqs * (((long long)max_q * g + rows_block - 1) / rows_block)
+                                                        : (long long)Tq * g / rows_block + (n_seqs + 1) / 2;
+    n_items = n_items < n_seqs ? n_seqs : (n_items > pl.items ? pl.items : n_items);
+    plan_long(&pl, n_items * (g > 1 ? Hkv : Hq), Tq, n_seqs, max_q, Hq, max_kv, rows_block, c->d);
     // Codes expanded once for all query blocks, or by every block for itself, by the
     // rows of a sequence.  Measured on 4 sequences of up to 8192 keys, us by blocks /
     // with the pass: d = 128 (32/8 heads) 512 rows 114 / 128, 1024 rows 182 / 179,
@@ -229,8 +257,21 @@ PagedPlan paged_plan(const attn_kv_cache_t* c, int Tq, int n_seqs, int max_q, in
     pl.blocks = (int)(segments * units < most ? segments * units : most);
   return pl;
 }
+// The list of pieces and what long_combine_kernel finds them by.
+struct PieceSpace {
+  long long pieces, list, lin, first;  // entries of the list; bytes
+};
+PieceSpace piece_space(long long n_seqs, long long items, int nh) {
+  PieceSpace s;
+  s.pieces = items * nh + kSms;  // (every cut adds one)
+  s.list = (4 * kPlanPiece * s.pieces + 15) / 16 * 16;
+  s.lin = 8 * (items + 2);
+  s.first = 4 * (n_seqs + 1);
+  return s;
+}
 // Workspace.  paged_fwd_kernel: a long long per sequence and one, the partial
-// rows, their LSE (nothing for clusters).  tcgen05: the item list, the windows' partial rows, their LSE.
+// rows, their LSE (nothing for clusters).  tcgen05: the list of items or pieces (and
+// the places of their tiles), the pieces' or windows' partial rows, their LSE.
 struct PagedSpace {
   long long head, o, lse, kv;  // bytes of each (kv: keys, and as much again for values)
   long long all() const { return head + o + lse + 2 * kv; }
@@ -239,10 +280,18 @@ PagedSpace paged_space(const PagedPlan& pl, long long Tq, long long n_seqs, long
   auto round = [](long long b) { return (b + 255) / 256 * 256; };
   PagedSpace s = {};
   if (pl.items > 0) {
-    s.head = ragged_plan_bytes(n_seqs, pl.items, (int)(ragged_rows_per_token((int)Hq, (int)Hkv) > 1 ? Hkv : Hq));
-    if (pl.n_windows > 1) {
-      s.o = round(pl.n_windows * Tq * Hq * d * 4);
-      s.lse = round(pl.n_windows * Tq * Hq * 4);
+    const int nh = (int)(ragged_rows_per_token((int)Hq, (int)Hkv) > 1 ? Hkv : Hq);
+    if (pl.pieces) {
+      const PieceSpace ps = piece_space(n_seqs, pl.items, nh);
+      s.head = round(ps.list + ps.lin + ps.first);
+      s.o = 2ll * kSms * ragged_block_rows((int)d, false) * d * 4;
+      s.lse = round(2ll * kSms * ragged_block_rows((int)d, false) * 4);
+    } else {
+      s.head = ragged_plan_bytes(n_seqs, pl.items, nh);
+      if (pl.n_windows > 1) {
+        s.o = round(pl.n_windows * Tq * Hq * d * 4);
+        s.lse = round(pl.n_windows * Tq * Hq * 4);
+      }
     }
     s.kv = n_seqs * pl.expand * Hkv * d * 2;
     return s;
@@ -302,13 +351,12 @@ int launch_paged_size(const PagedParams& p, const PagedPlan& pl, const attn_kv_c
 // A kernel that is launched while the one before it in the stream still runs and
 // waits for that one's results on the device, so its launch overlaps it.
 template <class... Args>
-int launch_dependent(void (*kernel)(Args...), long long blocks, int threads, size_t smem, cudaStream_t s, Args... args) {
-  if (blocks > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;
+int launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -323,7 +371,8 @@ int launch_paged(const PagedParams& p, const PagedPlan& pl, const attn_kv_cache_
   if (rc != ATTN_OK || pl.cluster || p.max_kv <= pl.unit) return rc;  // (a segment of one unit is never shared)
   const long long blocks = ((long long)p.Tq * p.Hq + 7) / 8;
   ATTN_LOGF("attn: paged_combine_kernel<%d> grid=(%lld) block=256 Tq=%d Hq=%d\n", D, blocks, p.Tq, p.Hq);
-  return launch_dependent(paged_combine_kernel<D>, blocks, 256, 0, s, p, pl.block_rows, pl.unit, pl.blocks);
+  if (blocks > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;
+  return launch_dependent(paged_combine_kernel<D>, dim3((unsigned)blocks), 256, 0, s, p, pl.block_rows, pl.unit, pl.blocks);
 }
 
 // ---------------------------------------------------------------- packed sequences on tcgen05
@@ -371,6 +420,7 @@ struct RaggedCall {
   const attn_kv_cache_t* cache;  // paged
   bool causal;
   float scale;
+  bool pieces;
   int n_windows, window;
   float *o_part, *lse_part;
   int* plan;
@@ -384,7 +434,8 @@ int launch_ragged(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
   const int g = ragged_rows_per_token(c.Hq, c.Hkv);
   const long long items = ragged_max_items(c.Tq, c.n_seqs, c.Hq, c.Hkv, Cfg::BM * Cfg::NQT);
   const int nh = g > 1 ? c.Hkv : c.Hq;
-  const long long blocks = items * nh * c.n_windows;
+  const PieceSpace ps = piece_space(c.n_seqs, items, nh);
+  const long long blocks = c.pieces ? ps.pieces : items * nh * c.n_windows;
   if (blocks > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;
   CUtensorMap tq, tk, tv;
   rc = g > 1 ? encode_packed_groups(&tq, c.q, c.Tq, c.Hq, g, c.d, c.q_stride, Cfg::BM)
@@ -407,7 +458,7 @@ int launch_ragged(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
       return ATTN_ERR_CUDA;
   }
   PlanParams pp;
-  pp.plan = ragged_listed(c.n_seqs, items, nh) ? c.plan : nullptr;
+  pp.plan = c.pieces || ragged_listed(c.n_seqs, items, nh) ? c.plan : nullptr;
   pp.max_items = (int)items;
   pp.n_seqs = c.n_seqs;
   pp.Tq = c.Tq;
@@ -423,7 +474,19 @@ int launch_ragged(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
   pp.bn = Cfg::BN;
   pp.causal = c.causal;
   pp.err = st->err;
-  if (pp.plan != nullptr) {
+  if (c.pieces) {
+    PiecePlanParams pc;
+    pc.seqs = pp;
+    pc.max_pieces = (int)ps.pieces;
+    pc.nh = nh;
+    pc.runs = kSms;
+    pc.min_share = 512 / Cfg::BN;
+    pc.lin = reinterpret_cast<long long*>(reinterpret_cast<char*>(c.plan) + ps.list);
+    pc.first = reinterpret_cast<int*>(reinterpret_cast<char*>(c.plan) + ps.list + ps.lin);
+    ATTN_LOGF("attn: piece_plan_kernel grid=(1) block=%d seqs=%d items<=%lld\n", kPlanThreads, c.n_seqs, items);
+    piece_plan_kernel<<<1, kPlanThreads, 0, s>>>(pc);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  } else if (pp.plan != nullptr) {
     ATTN_LOGF("attn: ragged_plan_kernel grid=(1) block=%d seqs=%d items<=%lld\n", kPlanThreads, c.n_seqs, items);
     ragged_plan_kernel<<<1, kPlanThreads, 0, s>>>(pp);
     if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
@@ -444,7 +507,7 @@ int launch_ragged(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
   p.sl2 = c.scale * 1.4426950408889634f;
   p.n_splits = c.n_windows;
   p.kv_chunk = c.n_windows > 1 ? c.window : 0x7FFFFFFF;
-  p.o_part = c.n_windows > 1 ? c.o_part : nullptr;
+  p.o_part = c.o_part;
   p.lse_part = c.lse_part;
   p.err = st->err;
   p.timeout_ns = timeout_ns();
@@ -453,6 +516,7 @@ int launch_ragged(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
   long long band = (48ll << 20) / (kv_head > 0 ? kv_head : 1);
   p.band = (int)(band < 1 ? 1 : (band > nh ? nh : band));
   p.rg.seqs = pp;
+  p.rg.pieces = c.pieces;
   p.rg.table = c.table;
   p.rg.table_width = c.table_width;
   p.rg.page_shift = c.cache != nullptr ? page_shift(c.cache) : 0;
@@ -462,8 +526,9 @@ int launch_ragged(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
   const dim3 grid((unsigned)blocks);
   if (log_on()) {
     char extra[96];
-    std::snprintf(extra, sizeof extra, " packed sequences%s windows=%d x %d pack=%d band=%d",
-                  Cfg::RAGGED == 1 ? "" : (Cfg::KV8 ? " (paged e4m3)" : " (paged)"), c.n_windows, c.window, g, p.band);
+    std::snprintf(extra, sizeof extra, " packed sequences%s%s windows=%d pack=%d band=%d",
+                  Cfg::RAGGED == 1 ? "" : (Cfg::KV8 ? " (paged e4m3)" : " (paged)"), c.pieces ? " pieces" : "",
+                  c.n_windows, g, p.band);
     log_launch<Cfg>("attn_fwd_kernel", grid, c.n_seqs, c.Hq, c.Hkv, c.Tq, c.Tk, extra);
   }
   if (pp.plan == nullptr) {
@@ -471,7 +536,7 @@ int launch_ragged(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
   }
   // (the launch overlaps the list's kernel, which the attention kernel waits for)
-  return launch_dependent(attn_fwd_kernel<Cfg>, blocks, Cfg::NTHREADS, Cfg::SMEM_BYTES, s, tq, tk, tv, (const FwdParams)p);
+  return launch_dependent(attn_fwd_kernel<Cfg>, grid, Cfg::NTHREADS, Cfg::SMEM_BYTES, s, tq, tk, tv, (const FwdParams)p);
 }
 template <int R>
 int launch_ragged_d(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
@@ -761,6 +826,7 @@ int attn_fwd_paged(const void* q, const attn_kv_cache_t* cache, void* o, float* 
     c.cache = cache;
     c.causal = causal != 0;
     c.scale = scale;
+    c.pieces = pl.pieces;
     c.n_windows = pl.n_windows;
     c.window = pl.window;
     c.o_part = o_part;
@@ -783,22 +849,30 @@ int attn_fwd_paged(const void* q, const attn_kv_cache_t* cache, void* o, float* 
     } else {
       rc = cache->dtype == ATTN_FP8_E4M3 ? launch_ragged_d<3>(c, st, s) : launch_ragged_d<2>(c, st, s);
     }
-    if (rc != ATTN_OK || pl.n_windows == 1) return rc;
-    WindowParams wp;
+    if (rc != ATTN_OK || (!pl.pieces && pl.n_windows == 1)) return rc;
+    LongParams wp;
     static_cast<PagedSeqs&>(wp) = seqs;
     wp.o = static_cast<__nv_bfloat16*>(o);
     wp.lse = lse;
     wp.Hq = Hq;
-    wp.window = pl.window;
+    wp.window = pl.pieces ? 0 : pl.window;
+    wp.rows_per_token = ragged_rows_per_token(Hq, cache->Hkv);
+    wp.block_rows = ragged_block_rows(d, false);
+    wp.nh = wp.rows_per_token > 1 ? cache->Hkv : Hq;
+    wp.max_items = (int)pl.items;
+    const PieceSpace ps = piece_space(n_seqs, pl.items, wp.nh);
+    wp.lin = reinterpret_cast<const long long*>(ws + ps.list);
+    wp.first = reinterpret_cast<const int*>(ws + ps.list + ps.lin);
     wp.o_part = o_part;
     wp.lse_part = lse_part;
-    const long long blocks = ((long long)Tq * Hq + 7) / 8;
-    ATTN_LOGF("attn: window_combine_kernel<%d> grid=(%lld) block=256 Tq=%d Hq=%d windows=%d\n", d, blocks, Tq, Hq,
-              pl.n_windows);
+    // a block per token, or more in a short call, whose heads are spread
+    const int sets = (Hq + 7) / 8, spread = 4 * kSms / Tq;
+    const dim3 grid((unsigned)Tq, (unsigned)(spread < 1 ? 1 : (spread > sets ? sets : spread)));
+    ATTN_LOGF("attn: long_combine_kernel<%d> grid=(%u,%u) block=256 Tq=%d Hq=%d\n", d, grid.x, grid.y, Tq, Hq);
     switch (d) {
-      case 64: return launch_dependent(window_combine_kernel<64>, blocks, 256, 0, s, (const WindowParams)wp);
-      case 128: return launch_dependent(window_combine_kernel<128>, blocks, 256, 0, s, (const WindowParams)wp);
-      default: return launch_dependent(window_combine_kernel<256>, blocks, 256, 0, s, (const WindowParams)wp);
+      case 64: return launch_dependent(long_combine_kernel<64>, grid, 256, 0, s, (const LongParams)wp);
+      case 128: return launch_dependent(long_combine_kernel<128>, grid, 256, 0, s, (const LongParams)wp);
+      default: return launch_dependent(long_combine_kernel<256>, grid, 256, 0, s, (const LongParams)wp);
     }
   }
   PagedParams p;

@@ -585,3 +585,84 @@ def test_prompt_step_captured_and_replayed():
         ref = su.attention(x[which][:, :Hq], k, v, True, 1 / math.sqrt(d))
         su.check_attention(o, lse, ref, d)
         su.check_attention(o1, l1, su.attention(x[which][-1:, :Hq], k, v, True, 1 / math.sqrt(d)), d)
+
+
+PIECES = [  # Hq, Hkv, d, new tokens, cached tokens, page size
+    (32, 8, 128, [256, 100, 130, 300], [6000, 2500, 4100, 300], 16),
+    (24, 8, 128, [300, 70, 1], [5000, 900, 64], 64),     # a group of 3: heads not stacked
+    (12, 12, 64, [700, 33, 0, 256], [4000, 50, 77, 3000], 32),
+    (16, 8, 256, [200, 90], [3000, 2600], 16),
+    (32, 8, 128, [513, 100, 65], [400, 20, 0], 128),     # rows that see no key, and a sequence without any
+]
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("case", range(len(PIECES)))
+def test_paged_pieces(case, e4m3, causal):
+    """Chunks whose key tiles are cut into one equal run per SM: by a table with room for long sequences, of which
+    some are short; captured, and replayed with other lengths and boundaries."""
+    torch, ea, su = setup()
+    Hq, Hkv, d, new, cached, page = PIECES[case]
+    n, T, top = len(new), sum(new), 16384
+    cache, table, ks, vs = su.make_cache(ea, cached, page, Hkv, d, e4m3, seed=case, width=top // page)
+    q = rand(torch, T, Hq, d, seed=case)
+    cu, lens = su.starts(new), su.i32(*cached)
+    # the workspace of pieces: their list, the places of the items' tiles, two partial blocks an SM, and rows of an
+    # expanded cache
+    g, rows = (Hq // Hkv if Hq // Hkv != 3 else 1), 128 if d == 256 else 256
+    items, nh = (T * g + n * (rows - 1)) // rows, Hkv if g > 1 else Hq
+    up = lambda x, to=256: (x + to - 1) // to * to
+    want = (up(up(48 * (items * nh + 148), 16) + 8 * (items + 2) + 4 * (n + 1)) + 296 * rows * d * 4 + up(296 * rows * 4))
+    if e4m3 and d > 64 and max(new) * (Hq // Hkv) >= (1024 if d == 128 else 512):
+        want += 2 * n * top * Hkv * d * 2
+    assert ea.attn_fwd_paged_workspace_bytes(cache.struct, T, n, max(new), Hq, top) == want
+    o, lse = torch.empty_like(q), torch.empty(Hq, T, device="cuda")
+
+    def check(new, cached):
+        a = 0
+        for s, (i, m) in enumerate(zip(new, cached)):
+            r = slice(a, a + i)
+            if i:
+                su.check_attention(o[r], lse[:, r], su.attention(q[r], ks[s][:m], vs[s][:m], causal, 1 / math.sqrt(d)), d)
+            a += i
+
+    def call():
+        ea.attention_paged(q, cache, table, lens, cu_q=cu, max_q=max(new), causal=causal, o=o, lse=lse)
+
+    call()
+    su.no_device_error(ea)
+    check(new, cached)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    other = [max(m - 37 * (s + 1), 0) for s, m in enumerate(cached)]
+    moved = new[:]
+    moved[0], moved[1] = new[0] - 17, new[1] + 9
+    lens.copy_(su.i32(*other))
+    cu.copy_(su.starts(moved))
+    o.fill_(7.0)
+    graph.replay()
+    su.no_device_error(ea)
+    check(moved, other)
+    assert bool((o[sum(moved):] == 7).all())  # rows behind the last sequence
+
+
+def test_pieces_of_bad_boundaries():
+    """Boundaries that overlap, so that the items are more than there can be: reported, and the next call is right."""
+    torch, ea, su = setup()
+    new, cached = [300, 70, 200], [3000, 900, 2000]
+    cache, table, ks, vs = su.make_cache(ea, cached, 32, 8, 128, False, seed=3, width=512)
+    q = rand(torch, 570, 32, 128, seed=1)
+    lens = su.i32(*cached)
+    for cu in (su.i32(0, 570, 0, 570), su.i32(0, 700, 300, 570), su.i32(-5, 100, 570, 100)):
+        ea.attention_paged(q, cache, table, lens, cu_q=cu, max_q=570)
+        assert ea.attn_get_last_device_error()[0] == 6
+    o, lse = ea.attention_paged(q, cache, table, lens, cu_q=su.starts(new), max_q=300)
+    su.no_device_error(ea)
+    su.check_attention(o[370:], lse[:, 370:], su.attention(q[370:], ks[2], vs[2], True, 1 / math.sqrt(128)), 128)
