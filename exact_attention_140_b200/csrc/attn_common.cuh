@@ -4,6 +4,7 @@
 #pragma once
 #include <cuda.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "ptx.cuh"
 #include "ragged_pick.cuh"
@@ -60,6 +61,8 @@ struct FwdParams {
   const float* dv;
   unsigned int* err;            // device error word
   unsigned long long timeout_ns;
+};
+struct RaggedFwdParams : FwdParams {
   RaggedParams rg;
 };
 
@@ -98,6 +101,7 @@ template <int D_, int BN_, int NQT_, int KST_, int VST_, bool CAUSAL_, bool FP8_
           int SB_ = (NQT_ == 1 ? 2 : 1), bool PSEP_ = false, int NS_ = 1, bool PACK_ = false, bool OST_ = false,
           int RAGGED_ = 0>
 struct FwdCfg {
+  using Params = std::conditional_t<RAGGED_ != 0, RaggedFwdParams, FwdParams>;
   // RAGGED (one-block-per-item kernel): 1 packed sequences, 2 packed queries
   // over a paged bf16 cache, 3 over a paged e4m3 cache (KV8: the codes arrive in
   // a ring of their own and a warpgroup expands them into the bf16 key and value

@@ -66,7 +66,7 @@ namespace attn {
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
+                    const __grid_constant__ CUtensorMap tmV, const typename Cfg::Params p) {
   constexpr int BM = Cfg::BM, BN = Cfg::BN, D = Cfg::D, NQT = Cfg::NQT, SB = Cfg::SB;
   static_assert(!Cfg::PSEP, "P overwrites S in this kernel");
   constexpr int KST = Cfg::KST, VST = Cfg::VST;
@@ -547,15 +547,18 @@ __global__ void __launch_bounds__(Cfg::NTHREADS, Cfg::BPS)
       // the page that holds this lane's rows of tile j; the index n_pages (a
       // box outside the map: zeros) behind the sequence and for a bad page
       auto page_of = [&](int j) -> int {
-        if constexpr (!PAGED) return 0;
-        const int ps = 1 << p.rg.page_shift, rows = ps < BN ? ps : BN;
-        const int key = kv0 + j * BN + lane * rows;
-        if (lane >= BN / rows || j * BN + lane * rows >= nk) return p.rg.n_pages;
-        const int pi = key >> p.rg.page_shift;
-        const int id = pi < p.rg.table_width ? __ldg(p.rg.table + (long long)seq * p.rg.table_width + pi) : -1;
-        if (id >= 0 && id < p.rg.n_pages) return id;
-        atomicOr(p.err, kErrIndex);
-        return p.rg.n_pages;
+        if constexpr (PAGED) {
+          const int ps = 1 << p.rg.page_shift, rows = ps < BN ? ps : BN;
+          const int key = kv0 + j * BN + lane * rows;
+          if (lane >= BN / rows || j * BN + lane * rows >= nk) return p.rg.n_pages;
+          const int pi = key >> p.rg.page_shift;
+          const int id = pi < p.rg.table_width ? __ldg(p.rg.table + (long long)seq * p.rg.table_width + pi) : -1;
+          if (id >= 0 && id < p.rg.n_pages) return id;
+          atomicOr(p.err, kErrIndex);
+          return p.rg.n_pages;
+        } else {
+          return 0;
+        }
       };
       [[maybe_unused]] int page = page_of(0);
       for (int j = 0; j < nmax; ++j) {

@@ -492,7 +492,7 @@ int launch_ragged(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
     if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   }
 
-  FwdParams p = {};
+  RaggedFwdParams p = {};
   p.o = c.o;
   p.lse = c.lse;
   p.B = 1;
@@ -536,7 +536,7 @@ int launch_ragged(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
   }
   // (the launch overlaps the list's kernel, which the attention kernel waits for)
-  return launch_dependent(attn_fwd_kernel<Cfg>, grid, Cfg::NTHREADS, Cfg::SMEM_BYTES, s, tq, tk, tv, (const FwdParams)p);
+  return launch_dependent(attn_fwd_kernel<Cfg>, grid, Cfg::NTHREADS, Cfg::SMEM_BYTES, s, tq, tk, tv, (const RaggedFwdParams)p);
 }
 template <int R>
 int launch_ragged_d(const RaggedCall& c, DeviceState* st, cudaStream_t s) {
